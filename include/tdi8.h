@@ -340,6 +340,68 @@ int conv2d_validate(int N, int H, int W, int C, int K, int R, int S,
                     int pad_h, int pad_w, int stride_h, int stride_w, int dil_h, int dil_w,
                     const int8_t *x, const int8_t *w, const int32_t *y);
 
+/* ---- 8-bit operands of a layer: norm and gated activation ----------------------
+ *
+ * The int8 operand of a product comes from a layer's activations: a row of
+ * values y becomes 8-bit values q and a scale, y ~ q * scale, and the product
+ * of the q is multiplied by the scales (gemm_s8s8_grouped, gemm_f8f8_block128).
+ * Two formats:
+ *   s8  int8 with one scale per row: scale = max|y| / 127, q = y / scale
+ *       rounded to the nearest integer, ties to even;
+ *   f8  8-bit floating point (e4m3: 4 exponent and 3 mantissa bits, largest
+ *       value 448, no infinity) with one scale per row and block of 128
+ *       columns (the last block may be shorter): scale = max|y| / 448.
+ * s8 rows are exact: q is the integer nearest to the real quotient, whatever
+ * the order of the sums (values next to a border between two integers are
+ * decided in 64 bits) and scale is computed in 64 bits and rounded once.  f8
+ * rows take their values in 32 bits: the quotient that is rounded to e4m3 is
+ * off by less than 2^-19, the scale by less than 2^-20 (relative).
+ * A row (f8: a block) of zeros gets q = 0 and scale = 0; one that holds an
+ * infinity or NaN gets q = 0 and scale = NaN.
+ *
+ * Types of x, residual, weight, sum, gate and up: */
+typedef enum {
+    TDI8_F32 = 0,
+    TDI8_BF16 = 1,
+    TDI8_F16 = 2
+} tdi8_type;
+
+/* RMS norm of T rows of H columns with the residual's addition, s8 output:
+ *   h = x + residual, rounded to `type` (h = x without a residual),
+ *   y[i][j] = h[i][j] * weight[j] / sqrt(mean over j of h[i][j]^2 + eps),
+ * q (T x H int8, leading dimension ldq) and scale (T floats) the s8 form of
+ * y, and sum (T x H, leading dimension ldsum) = h, the residual stream that
+ * the next layer adds to.  The norm is taken of the rounded h, so that it is
+ * the norm of what the stream holds.  Sums are held in 64 bits.
+ * residual may be NULL (sum must be NULL then); sum may be NULL, or x or
+ * residual itself (same pointer and leading dimension; in place), but no
+ * output may overlap an input or another output otherwise (TDI8_ERR_ALIASING).
+ * Pointers to `type` are aligned to its size, scale to 4 bytes; leading
+ * dimensions are in elements, at least H, and H is at most 2^30
+ * (TDI8_ERR_INVALID_VALUE otherwise, also for eps < 0 or not finite and an
+ * unknown type).  T == 0 or H == 0 enqueues nothing.  One kernel on `stream`;
+ * ownership and the other errors as for gemm_s8s8s32. */
+int rmsnorm_quant_s8(int type, int T, int H, const void *x, int ldx, const void *residual, int ldr,
+                     const void *weight, float eps, void *sum, int ldsum, int8_t *q, int ldq, float *scale,
+                     hipStream_t stream);
+
+/* The same with f8 output: q holds e4m3 bytes, scale T rows of
+ * ceil(H / 128) floats (leading dimension lds >= ceil(H / 128)). */
+int rmsnorm_quant_f8(int type, int T, int H, const void *x, int ldx, const void *residual, int ldr,
+                     const void *weight, float eps, void *sum, int ldsum, uint8_t *q, int ldq, float *scale,
+                     int lds, hipStream_t stream);
+
+/* Gated activation of T rows of N columns, s8 output:
+ *   y[i][j] = gate[i][j] / (1 + exp(-gate[i][j])) * up[i][j].
+ * gate and up may be the two halves of one product's rows (leading
+ * dimensions at least N).  Outputs, checks and errors as for the norm. */
+int swiglu_quant_s8(int type, int T, int N, const void *gate, int ldg, const void *up, int ldu, int8_t *q,
+                    int ldq, float *scale, hipStream_t stream);
+
+/* The same with f8 output. */
+int swiglu_quant_f8(int type, int T, int N, const void *gate, int ldg, const void *up, int ldu, uint8_t *q,
+                    int ldq, float *scale, int lds, hipStream_t stream);
+
 /* Host-side argument check shared by every gemm entry point (no device
  * needed): returns TDI8_OK or the status the entry point would return. */
 int tdi8_validate(int b_col_major, int M, int N, int K, const int8_t *A, int lda,

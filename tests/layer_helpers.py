@@ -1,0 +1,83 @@
+"""Plain 64-bit forms of the 8-bit layer operators and tensors for their tests."""
+from __future__ import annotations
+
+import torch
+
+BLOCK = 128
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def strided(t, ld=None, offset=0):
+    """t's values in a larger buffer on the GPU: rows `ld` elements apart,
+    the first one `offset` elements in.  Returns (view, whole buffer)."""
+    rows, cols = t.shape
+    ld = cols if ld is None else ld
+    buf = torch.full((offset + rows * ld + 16,), 7, dtype=torch.int8, device="cuda").to(t.dtype)
+    view = buf[offset:offset + rows * ld].view(rows, ld)[:, :cols]
+    view.copy_(t.cuda())
+    return view, buf
+
+
+def norm_sum(x, residual):
+    """x + residual as the operator rounds it (CPU)."""
+    return x if residual is None else (x.float() + residual.float()).to(x.dtype)
+
+
+def norm_values(x, weight, residual, eps):
+    """(v, inv): v = h w and the row's 1 / root, in 64 bits on the CPU."""
+    h = norm_sum(x, residual).double()
+    inv = 1 / torch.sqrt((h * h).mean(1) + eps)
+    return h * weight.double(), inv
+
+
+def norm_steps(x):
+    """check_quantised's `steps` of the norm of x."""
+    return 1 if x.dtype == torch.float32 else 0
+
+
+def act_values(gate, up):
+    g = gate.double()
+    v = g / (1 + torch.exp(-g)) * up.double()
+    return v, torch.ones(gate.shape[0], dtype=torch.float64)
+
+
+def quantise(v, inv, fmt):
+    """(quotients in 64 bits, scales in 64 bits) of finite rows v."""
+    T, H = v.shape
+    top, width = (127.0, max(H, 1)) if fmt == "s8" else (448.0, BLOCK)
+    quotients, scales = torch.zeros_like(v), []
+    for c in range(0, H, width):
+        part = v[:, c:c + width]
+        m = part.abs().amax(1, keepdim=True)
+        quotients[:, c:c + width] = torch.where(m > 0, part * top / m, torch.zeros_like(part))
+        scales.append(torch.where(m[:, 0] > 0, m[:, 0] * inv / top, torch.zeros_like(inv)))
+    return quotients, torch.stack(scales, 1)
+
+
+def check_quantised(q, scale, v, inv, fmt, what, steps=10):
+    """q and scale against the quotients in 64 bits.
+
+    `steps`: by how many times 2^-24 a 32-bit value v may be off (relative):
+    10 for the activation, 1 for the norm's product of 32-bit values, 0 for
+    that of 16-bit values, which is exact in 32 bits.
+    s8: equal to the nearest integer, ties to even; the scale is computed in
+    64 bits and rounded once to fp32, half a step = 2^-24 relative (values in
+    fp32's normal range), plus what two 64-bit computations differ by
+    (< 2^-40).
+    f8: the largest value of a block is a 32-bit one, so the scale is off by
+    `steps` more; the quotient v * (448 / largest) by that twice and its two
+    operations: at most 22 * 2^-24 < 2^-19.  q is the e4m3 value of a
+    quotient that near to the exact one."""
+    t, want = quantise(v, inv, fmt)
+    if fmt == "s8":
+        bad = (q.cpu().double() != t.round()).nonzero()
+        assert not len(bad), f"{what}: {len(bad)} values differ, first at {bad[0].tolist()}"
+        scale = scale.reshape(-1, 1)
+    else:
+        got = q.cpu().float()
+        near = [(t * (1 + d)).float().clamp(-448, 448).to(torch.float8_e4m3fn).float() for d in (-2.0 ** -19, 0, 2.0 ** -19)]
+        ok = (got == near[0]) | (got == near[1]) | (got == near[2])
+        assert ok.all(), f"{what}: {(~ok).sum()} values differ, first at {(~ok).nonzero()[0].tolist()}"
+    off = (scale.cpu().double() - want).abs()
+    allowed = 2.0 ** -24 * (1 + (steps if fmt == "f8" else 0)) + 2.0 ** -40
+    assert (off <= want * allowed).all(), f"{what}: scales off by {(off / want).max()}"

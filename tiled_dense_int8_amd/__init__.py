@@ -31,6 +31,8 @@ ERR_UNSUPPORTED_DEVICE = -4
 ERR_BAD_CONFIG = -5
 ERR_HIP = -6
 
+F32, BF16, F16 = 0, 1, 2  # tdi8_type
+
 ROUTE_GENERAL, ROUTE_FALLBACK, ROUTE_SKINNY = 0, 1, 2
 
 
@@ -66,7 +68,7 @@ class Plan(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
-_i, _p = ctypes.c_int, ctypes.c_void_p
+_i, _p, _f = ctypes.c_int, ctypes.c_void_p, ctypes.c_float
 _GEMM_ARGS = [_i, _i, _i, _p, _i, _p, _i, _p, _i, _p]
 _SIGNATURES = {
     "gemm_s8s8s32": (_i, _GEMM_ARGS),
@@ -86,14 +88,18 @@ _SIGNATURES = {
     "conv2d_select_config": (_i, [_i] * 13),
     "conv2d_output_extent": (_i, [_i] * 5),
     "conv2d_validate": (_i, [_i] * 13 + [_p, _p, _p]),
+    "rmsnorm_quant_s8": (_i, [_i] * 3 + [_p, _i, _p, _i, _p, _f, _p, _i, _p, _i, _p, _p]),
+    "rmsnorm_quant_f8": (_i, [_i] * 3 + [_p, _i, _p, _i, _p, _f, _p, _i, _p, _i, _p, _i, _p]),
+    "swiglu_quant_s8": (_i, [_i] * 3 + [_p, _i, _p, _i, _p, _i, _p, _p]),
+    "swiglu_quant_f8": (_i, [_i] * 3 + [_p, _i, _p, _i, _p, _i, _p, _i, _p]),
     "tdi8_status_string": (ctypes.c_char_p, [_i]),
     "tdi8_last_hip_error": (_i, []),
     "tdi8_kernel_code_hash": (ctypes.c_char_p, []),
 }
 for _name, (_res, _args) in _SIGNATURES.items():
-    _f = getattr(_lib, _name)
-    _f.restype = _res
-    _f.argtypes = _args
+    _fn = getattr(_lib, _name)
+    _fn.restype = _res
+    _fn.argtypes = _args
 
 EXPORTED = tuple(_SIGNATURES)
 
@@ -341,3 +347,144 @@ def conv2d(x, w, pad=(0, 0), stride=(1, 1), dil=(1, 1), out=None, config=None, s
     if st != OK:
         raise TDI8Error(st)
     return out
+
+
+# ---- 8-bit operands of a layer: norm and gated activation ---------------------------
+
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+BLOCK = 128  # columns that share a scale in the f8 format
+
+
+def rmsnorm_quant_s8(type, T, H, x, ldx, residual, ldr, weight, eps, sum, ldsum, q, ldq, scale, stream=0) -> int:
+    _int32(type=type, T=T, H=H, ldx=ldx, ldr=ldr, ldsum=ldsum, ldq=ldq)
+    return _lib.rmsnorm_quant_s8(type, T, H, x, ldx, residual, ldr, weight, eps, sum, ldsum, q, ldq, scale, stream)
+
+
+def rmsnorm_quant_f8(type, T, H, x, ldx, residual, ldr, weight, eps, sum, ldsum, q, ldq, scale, lds,
+                     stream=0) -> int:
+    _int32(type=type, T=T, H=H, ldx=ldx, ldr=ldr, ldsum=ldsum, ldq=ldq, lds=lds)
+    return _lib.rmsnorm_quant_f8(type, T, H, x, ldx, residual, ldr, weight, eps, sum, ldsum, q, ldq, scale, lds,
+                                 stream)
+
+
+def swiglu_quant_s8(type, T, N, gate, ldg, up, ldu, q, ldq, scale, stream=0) -> int:
+    _int32(type=type, T=T, N=N, ldg=ldg, ldu=ldu, ldq=ldq)
+    return _lib.swiglu_quant_s8(type, T, N, gate, ldg, up, ldu, q, ldq, scale, stream)
+
+
+def swiglu_quant_f8(type, T, N, gate, ldg, up, ldu, q, ldq, scale, lds, stream=0) -> int:
+    _int32(type=type, T=T, N=N, ldg=ldg, ldu=ldu, ldq=ldq, lds=lds)
+    return _lib.swiglu_quant_f8(type, T, N, gate, ldg, up, ldu, q, ldq, scale, lds, stream)
+
+
+def _call(dev, fn, *args, stream) -> None:
+    """fn(*args, stream handle) with the tensors' device current; raises TDI8Error."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream_handle(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream_handle(stream))
+    if st != OK:
+        raise TDI8Error(st)
+
+
+def _ld(t) -> int:
+    """Leading dimension of a 2-D tensor with unit column stride (a single row may have any)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _matrix(name, t, dtype, shape=None) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap")
+
+
+def _empty(shape, dtype, dev, stream):
+    """A new tensor of the stream that the call runs on (so that its memory
+    is not handed out again while the call still runs)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _eight_bit_out(fmt, T, H, dev, out, scale, stream):
+    """The 8-bit output and its scales: the caller's, checked, or new ones."""
+    if fmt not in ("s8", "f8"):
+        raise ValueError(f"fmt must be 's8' or 'f8', not {fmt!r}")
+    dtype, shape = (torch.int8, (T,)) if fmt == "s8" else (torch.float8_e4m3fn, (T, -(-H // BLOCK)))
+    if out is None:
+        out = _empty((T, H), dtype, dev, stream)
+    else:
+        _matrix("out", out, dtype, (T, H))
+    if scale is None:
+        scale = _empty(shape, torch.float32, dev, stream)
+    elif scale.dtype != torch.float32 or tuple(scale.shape) != shape or (shape[-1] > 1 and scale.stride(-1) != 1):
+        raise ValueError(f"scale must be float32 {shape} with unit stride along its last axis")
+    return out, scale
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, fmt: str = "s8", sum_out=None, out=None, scale=None,
+             stream=None):
+    """RMS norm of x (T, H) with an 8-bit output: (q, scale), or with a
+    residual (q, scale, sum) for the norm of sum = x + residual.
+
+    x, residual, weight (H): float32, bfloat16 or float16, all alike, with
+       unit column stride.
+    fmt: "s8": q int8 with scale (T); "f8": q float8_e4m3fn with scale
+       (T, ceil(H / 128)), one for each block of 128 columns.
+    sum_out: where the sum goes (x or residual itself: in place).
+    """
+    if x.dtype not in _TYPES:
+        raise TypeError("x must be float32, bfloat16 or float16")
+    _matrix("x", x, x.dtype)
+    T, H = x.shape
+    if weight.dtype != x.dtype or tuple(weight.shape) != (H,) or (H > 1 and weight.stride(0) != 1):
+        raise ValueError(f"weight must be a dense {x.dtype} vector of {H} values")
+    if residual is not None:
+        _matrix("residual", residual, x.dtype, (T, H))
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    given = [t for t in (x, weight, residual, sum_out, out, scale) if t is not None]
+    dev = _device_of(*given)
+    if residual is not None:
+        if sum_out is None:
+            sum_out = _empty((T, H), x.dtype, dev, stream)
+        else:
+            _matrix("sum_out", sum_out, x.dtype, (T, H))
+    out, scale = _eight_bit_out(fmt, T, H, dev, out, scale, stream)
+    args = [_TYPES[x.dtype], T, H, x.data_ptr(), _ld(x), residual.data_ptr() if residual is not None else None,
+            _ld(residual) if residual is not None else 0, weight.data_ptr(), eps,
+            sum_out.data_ptr() if residual is not None else None, _ld(sum_out) if residual is not None else 0,
+            out.data_ptr(), _ld(out), scale.data_ptr()]
+    if fmt == "s8":
+        _call(dev, rmsnorm_quant_s8, *args, stream=stream)
+    else:
+        _call(dev, rmsnorm_quant_f8, *args, _ld(scale), stream=stream)
+    return (out, scale) if residual is None else (out, scale, sum_out)
+
+
+def swiglu(gate, up, fmt: str = "s8", out=None, scale=None, stream=None):
+    """(q, scale) of gate / (1 + exp(-gate)) * up for gate and up (T, N), in
+    the formats of rms_norm; the two may be halves of one tensor's rows."""
+    if gate.dtype not in _TYPES:
+        raise TypeError("gate must be float32, bfloat16 or float16")
+    _matrix("gate", gate, gate.dtype)
+    T, N = gate.shape
+    _matrix("up", up, gate.dtype, (T, N))
+    dev = _device_of(*(t for t in (gate, up, out, scale) if t is not None))
+    out, scale = _eight_bit_out(fmt, T, N, dev, out, scale, stream)
+    args = [_TYPES[gate.dtype], T, N, gate.data_ptr(), _ld(gate), up.data_ptr(), _ld(up), out.data_ptr(), _ld(out),
+            scale.data_ptr()]
+    if fmt == "s8":
+        _call(dev, swiglu_quant_s8, *args, stream=stream)
+    else:
+        _call(dev, swiglu_quant_f8, *args, _ld(scale), stream=stream)
+    return out, scale

@@ -13,6 +13,7 @@
 #if defined(TDI8_STAMPS)
 #include "../../include/tdi8_stamps.h"
 #endif
+#include "abi_common.h"
 #include "kernel_table.h"
 #include "selector.h"
 #include "device_common.h"
@@ -38,14 +39,14 @@ __global__ void __launch_bounds__(256) zero_c_kernel(GemmArgs g) {
     }
 }
 
-namespace {
-
-thread_local int g_last_hip_error = 0;
+static thread_local int g_last_hip_error = 0;
 
 int hip_fail(hipError_t e) {
     g_last_hip_error = static_cast<int>(e);
     return TDI8_ERR_HIP;
 }
+
+namespace {
 
 #if defined(TDI8_STAMPS)
 // Timeline buffer of the instrumented library (tdi8_stamps_set).
@@ -147,8 +148,6 @@ DeviceState *current_device(int *status) {
     }
     return &ds;
 }
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Which kernel runs a call, on which grid: one decision, shared by the launch
 // and the gemm_plan query, so that what the query reports is what runs.
@@ -278,8 +277,6 @@ int run_plan(Plan &p, hipStream_t stream) {
     if (e != hipSuccess) return hip_fail(e);
     return TDI8_OK;
 }
-
-bool overlaps(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a0 < b1 && b0 < a1; }
 
 // The plan of a call: the given configuration, or (cfg -1) the selection's,
 // with the predicated column-major form moved to a configuration whose tiles
@@ -470,6 +467,14 @@ int conv_entry(int cfg, const ConvShape &c, const int8_t *x, const int8_t *w, in
 }
 
 }  // namespace
+
+int device_units(int *num_cu) {
+    int st = TDI8_OK;
+    DeviceState *ds = current_device(&st);
+    if (ds) *num_cu = ds->hw.num_cu;
+    return st;
+}
+
 }  // namespace tdi8
 
 using namespace tdi8;
