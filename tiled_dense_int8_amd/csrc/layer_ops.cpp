@@ -74,13 +74,22 @@ int rows_entry(int op, int fmt, int type, RowArgs g, hipStream_t stream) {
     int units = 0;
     st = device_units(&units);
     if (st != TDI8_OK) return st;
-    // the smallest shape that keeps the row in registers, else the one that reads it twice
-    int shape = 0;
-    while (shape + 1 < kRowShapes && kRowShape[shape].threads * kRowShape[shape].vectors * 8 < g.cols) ++shape;
+    // the smallest shape that keeps the row in registers, else the one that
+    // reads it twice; f8 activations need only whole blocks of 128 columns
+    // and take a row by blocks of at most kActShape
+    int shape = g.cols < 8 ? 0 : 1;
+    auto width = [](int s) { return kRowShape[s].threads * kRowShape[s].vectors * 8; };
+    const bool apart = op == kOpAct && fmt == kFmtF8;
+    while (shape > 0 && shape + 1 < kRowShapes && width(shape) < g.cols && !(apart && shape == kActShape)) ++shape;
+    unsigned parts = apart && shape > 0 ? (g.cols + width(shape) - 1) / width(shape) : 1;
+    if (parts > 65535) {  // the grid's limit
+        shape = kRowShapes - 1;
+        parts = 1;
+    }
     const int per = rows_per_block(kRowShape[shape].threads);
     const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(g.rows) + per - 1) / per);
     void *args[] = {&g};
-    const hipError_t e = hipLaunchKernel(row_kernels(type)->kernel[shape][op][fmt], dim3(blocks),
+    const hipError_t e = hipLaunchKernel(row_kernels(type)->kernel[shape][op][fmt], dim3(blocks, parts),
                                          dim3(kRowShape[shape].threads * per), args, 0, stream);
     return e == hipSuccess ? TDI8_OK : hip_fail(e);
 }

@@ -20,12 +20,17 @@ struct RowArgs {
 };
 
 // Row shapes: threads per row times vectors of 8 columns that a thread keeps
-// in registers; the last one keeps none and reads the row twice.
-enum { kRowShapes = 6 };
+// in registers.  The first (vectors < 0) takes rows shorter than 8 columns,
+// the last (0) keeps none and reads the row twice.
+enum { kRowShapes = 9 };
 struct RowShape {
     int threads, vectors;
 };
-constexpr RowShape kRowShape[kRowShapes] = {{64, 1}, {256, 1}, {256, 2}, {256, 4}, {1024, 2}, {1024, 0}};
+constexpr RowShape kRowShape[kRowShapes] = {{64, -1}, {64, 1},  {256, 1}, {256, 2}, {256, 3},
+                                            {256, 4}, {512, 3}, {512, 4}, {1024, 0}};
+// f8 activations, which need no whole row, take a longer one by blocks of this
+// shape (8192 x 11008: 108 us; one block of 1024 threads per row: 163 us).
+constexpr int kActShape = 3;  // {256, 2}
 // Rows that one block computes: the one-wave shape puts four in a block.
 constexpr int rows_per_block(int threads) { return threads == 64 ? 4 : 1; }
 

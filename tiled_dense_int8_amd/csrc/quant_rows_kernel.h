@@ -29,66 +29,143 @@
 // twice, the second time mostly from the cache), each thread holding vectors
 // of 8 columns, so a block of 128 columns is 16 neighbouring lanes and its
 // maximum needs no shared memory.
+//
+// Measured on MI355X (bytes read and written once over the time; a device
+// copy of 1 GiB runs at 5.2 TB/s): norm of 16384 x 8192 bf16 with a residual
+// 162 us (5.8 TB/s) s8, 160 us f8; 4096 x 16384 89 us (5.3 TB/s); 2048 x 20000,
+// read twice, 94 us (3.1 TB/s).  act of 8192 x 11008 bf16 118 us (3.8 TB/s)
+// s8, 106 us (4.3 TB/s) f8: there the exponential's instructions count.
 #pragma once
-
-#include <hip/hip_bf16.h>
-#include <hip/hip_fp16.h>
 
 #include "quant_rows.h"
 
 namespace tdi8 {
 
+// Eight elements as 32-bit words: one each for F32, two elements in each for
+// the 16-bit types.
+// kHalf: products of two magnitudes stay below 2^40.
 struct F32 {
-    using Raw = float;
-    static __device__ __forceinline__ float to_float(float v) { return v; }
-    static __device__ __forceinline__ float round(float v) { return v; }
+    static constexpr bool kHalf = false;
+    static constexpr int kBytes = 4;
+    typedef uint32_t Words __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ float get(const Words &w, int i) { return __uint_as_float(w[i]); }
+    static __device__ __forceinline__ void set2(Words &w, int i, float a, float b) {
+        w[i] = __float_as_uint(a);
+        w[i + 1] = __float_as_uint(b);
+    }
 };
 struct Bf16 {
-    using Raw = uint16_t;
-    static __device__ __forceinline__ float to_float(uint16_t v) { return __uint_as_float(uint32_t{v} << 16); }
-    // nearest, ties to even; NaN stays NaN
-    static __device__ __forceinline__ uint16_t round(float v) {
-        const uint32_t u = __float_as_uint(v);
-        if ((u & 0x7fffffffu) > 0x7f800000u) return static_cast<uint16_t>((u >> 16) | 0x40u);
-        return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+    static constexpr bool kHalf = false;
+    static constexpr int kBytes = 2;
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ float get(const Words &w, int i) {
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    // nearest, ties to even (v_cvt_pk_bf16_f32)
+    static __device__ __forceinline__ void set2(Words &w, int i, float a, float b) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+        w[i >> 1] = __builtin_bit_cast(uint32_t, v);
     }
 };
 struct F16 {
-    using Raw = uint16_t;
-    static __device__ __forceinline__ float to_float(uint16_t v) {
-        return static_cast<float>(__builtin_bit_cast(_Float16, v));
+    static constexpr bool kHalf = true;
+    static constexpr int kBytes = 2;
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ float get(const Words &w, int i) {
+        const uint32_t pair = w[i >> 1];
+        return static_cast<float>(__builtin_bit_cast(f16x2, pair)[i & 1]);
     }
-    static __device__ __forceinline__ uint16_t round(float v) {
-        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+    static __device__ __forceinline__ void set2(Words &w, int i, float a, float b) {
+        w[i >> 1] = __builtin_bit_cast(uint32_t, f16x2{static_cast<_Float16>(a), static_cast<_Float16>(b)});
     }
 };
 
 template <class T>
 struct Vec8 {
-    typename T::Raw e[8];
+    static constexpr int kWords = 2 * T::kBytes;
+    typename T::Words w;
+    __device__ __forceinline__ float get(int i) const { return T::get(w, i); }
+    // Element i of a run-time index, for paths that few rows take: a loop
+    // over it keeps them short.
+    __device__ __forceinline__ float pick(int i) const {
+        float v = get(0);
+#pragma unroll
+        for (int j = 1; j < 8; ++j) v = i == j ? get(j) : v;
+        return v;
+    }
 };
 
-// Eight elements at p (any alignment of p that its type allows; global memory
-// takes unaligned wide loads), or the first n of them and zeros.
+// The elements moved down by one, zero at the top.
 template <class T>
-__device__ __forceinline__ Vec8<T> load8(const typename T::Raw *p, int n) {
-    Vec8<T> v;
-    if (n >= 8) {
-        __builtin_memcpy(&v, p, sizeof(v));
-    } else {
+__device__ __forceinline__ void shift_down(Vec8<T> &v) {
+    constexpr int W = Vec8<T>::kWords;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.e[i] = i < n ? p[i] : typename T::Raw(0);
-    }
-    return v;
+    for (int j = 0; j + 1 < W; ++j) v.w[j] = T::kBytes == 4 ? v.w[j + 1] : v.w[j] >> 16 | v.w[j + 1] << 16;
+    v.w[W - 1] = T::kBytes == 4 ? 0u : v.w[W - 1] >> 16;
 }
+
+// Eight elements at p, at any alignment that their type allows (global memory
+// takes unaligned wide loads).
 template <class T>
-__device__ __forceinline__ void store8(typename T::Raw *p, const Vec8<T> &v, int n) {
-    if (n >= 8) {
-        __builtin_memcpy(p, &v, sizeof(v));
-    } else {
+__device__ __forceinline__ void load8(Vec8<T> &v, const char *p) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = v.e[i];
+    for (int h = 0; h < Vec8<T>::kWords / 4; ++h) {
+        u32x4 x;
+        __builtin_memcpy(&x, p + 16 * h, 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v.w[4 * h + j] = x[j];
+    }
+}
+// The first n < 8 elements at p and zeros, for rows shorter than 8.
+template <class T>
+__device__ __forceinline__ void load_few(Vec8<T> &v, const char *p, int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t e = 0;
+        if (i < n) {
+            if constexpr (T::kBytes == 4)
+                e = reinterpret_cast<const uint32_t *>(p)[i];
+            else
+                e = reinterpret_cast<const uint16_t *>(p)[i];
+        }
+        if constexpr (T::kBytes == 4)
+            v.w[i] = e;
+        else
+            v.w[i >> 1] = i & 1 ? v.w[i >> 1] | e << 16 : e;
+    }
+}
+// Eight elements to p, or the first n.
+template <class T>
+__device__ __forceinline__ void store8(char *p, Vec8<T> v, int n) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    if (n >= 8) {
+#pragma unroll
+        for (int h = 0; h < Vec8<T>::kWords / 4; ++h) {
+            const u32x4 x = {v.w[4 * h], v.w[4 * h + 1], v.w[4 * h + 2], v.w[4 * h + 3]};
+            __builtin_memcpy(p + 16 * h, &x, 16);
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            if constexpr (T::kBytes == 4)
+                reinterpret_cast<uint32_t *>(p)[i] = v.w[0];
+            else
+                reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(v.w[0]);
+            shift_down(v);
+        }
+    }
+}
+// Eight bytes at p, or the first n.
+__device__ __forceinline__ void store8_bytes(uint8_t *p, uint32_t lo, uint32_t hi, int n) {
+    uint64_t v = static_cast<uint64_t>(hi) << 32 | lo;
+    if (n >= 8) {
+        __builtin_memcpy(p, &v, 8);
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < n; ++i, v >>= 8) p[i] = static_cast<uint8_t>(v);
     }
 }
 
@@ -122,9 +199,10 @@ __device__ __forceinline__ double value64(float a, float b) {
 // The same in fp32.  act: relative error at most 10 * 2^-24 in the range
 // above: e^-g = 2^hi (1 + lo ln 2) with hi + lo = -g log2 e to twice the
 // precision (2^hi and the reciprocal are off by 2^-23 each, the other six
-// operations by 2^-24).  Below g = -80 the exponential may overflow; the
-// value is then at most 80 e^-80 |u|, nothing next to 2^-60 unless |u| is
-// huge: such a value is reported as out of range.
+// operations by 2^-24).  Below g = -80 it takes e^80, so that the exponential
+// cannot overflow; the value is then below 2 * 10^-35 |g u|, nothing next to
+// 2^-60 while |g u| is at most 2^40 (values32 sees to that).  NaN and
+// infinities come out as NaN or an infinity.
 template <int OP>
 __device__ __forceinline__ float value32(float a, float b) {
     if constexpr (OP == kOpNorm) {
@@ -132,14 +210,27 @@ __device__ __forceinline__ float value32(float a, float b) {
     } else {
         constexpr float kLog2e = 1.44269502162933349609375f;   // fp32 nearest to log2 e
         constexpr float kLog2eLo = 1.92596299112661746887e-8f;  // log2 e - kLog2e
-        const float hi = a * -kLog2e;
-        const float lo = __builtin_fmaf(a, -kLog2e, -hi) - a * kLog2eLo;
-        float e = __builtin_amdgcn_exp2f(hi);
-        e = hi < 120.0f ? __builtin_fmaf(e, lo * 0.693147182f, e) : e;
-        float v = a * __builtin_amdgcn_rcpf(1.0f + e) * b;
-        if (a < -80.0f) v = fabsf(b) > 1048576.0f ? __builtin_inff() : 0.0f;
-        return v + ((a - a) + (b - b));  // NaN where a or b is no finite number
+        const float g = fmaxf(a, -80.0f);
+        const float hi = g * -kLog2e;
+        const float lo = __builtin_fmaf(g, -kLog2eLo, __builtin_fmaf(g, -kLog2e, -hi));
+        const float e2 = __builtin_amdgcn_exp2f(hi);
+        const float e = __builtin_fmaf(e2, lo * 0.693147182f, e2);
+        return a * __builtin_amdgcn_rcpf(1.0f + e) * b;
     }
+}
+// Eight of them; one is an infinity where the fp32 form may not hold, which
+// sends the row (block) to the fp64 path.
+template <class T, int OP>
+__device__ __forceinline__ void values32(const Vec8<T> &a, const Vec8<T> &b, float *v) {
+    float am = 0.0f, bm = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = a.get(i), y = b.get(i);
+        v[i] = value32<OP>(x, y);
+        am = fmaxf(am, fabsf(x));
+        bm = fmaxf(bm, fabsf(y));
+    }
+    if constexpr (OP == kOpAct && !T::kHalf) v[0] = am * bm > 0x1p40f ? __builtin_inff() : v[0];
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
@@ -181,16 +272,24 @@ __device__ __forceinline__ float scale_of(double m, double inv, double top, bool
     return !number ? __builtin_nanf("") : m == 0.0 ? 0.0f : static_cast<float>(m * inv / top);
 }
 
-// How near a border the fp32 quotient counts as undecided.  Error of t = v k:
-// k = 127 / max|v| rounded once, the product once, v by at most 10 * 2^-24:
-// 12 * 2^-24 * 127 < 2^-13.
-constexpr float kNear = 0x1p-13f;
+// How near a border the fp32 quotient counts as undecided: above its error.
+// t = v k is rounded with its border test in one step (fused), so it is off by
+// 127 times the relative errors of v (at most 10 * 2^-24, 2^-24, 0 for the
+// activation, the norm of fp32, the norm of 16-bit types), of the maximum's
+// fp32 form (2^-24, exact for 16-bit products) and of k (2^-24):
+// 12, 3 and 1 times 127 * 2^-24.
+template <class T, int OP>
+constexpr float kNear = OP == kOpAct ? 0x1p-13f : T::kBytes == 4 ? 0x1p-15f : 0x1p-16f;
+// fp32 values from 2^22 up to 2^23 in magnitude plus this have their integer
+// part, rounded to nearest even, in the low mantissa bits.
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
 
 template <class T, int THREADS, int NV, int OP, int FMT>
 __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kernel(RowArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    using Raw = typename T::Raw;
+    constexpr int SIZE = T::kBytes;
     constexpr int WAVES = THREADS / 64;
+    constexpr bool FEW = NV < 0;  // rows shorter than 8: one wave each, its first thread holds them
     constexpr int KEEP = NV > 0 ? NV : 1;
     __shared__ double sh_sum[WAVES];
     __shared__ uint32_t sh_max[WAVES];
@@ -200,85 +299,158 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
     const int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block(THREADS) +
                         (THREADS == 64 ? threadIdx.x >> 6 : 0);
     if (row >= g.rows) return;  // whole waves of the one-wave shape, which has no barrier
-    const Raw *pa = static_cast<const Raw *>(g.a) + row * g.lda;
-    const Raw *pb = g.b ? static_cast<const Raw *>(g.b) + row * g.ldb : nullptr;
-    const Raw *pw = static_cast<const Raw *>(g.weight);
-    Raw *psum = g.sum ? static_cast<Raw *>(g.sum) + row * g.ldsum : nullptr;
+    const char *pa = static_cast<const char *>(g.a) + row * g.lda * SIZE;
+    const char *pb = g.b ? static_cast<const char *>(g.b) + row * g.ldb * SIZE : nullptr;
+    const char *pw = static_cast<const char *>(g.weight);
+    char *psum = g.sum ? static_cast<char *>(g.sum) + row * g.ldsum * SIZE : nullptr;
     uint8_t *pq = static_cast<uint8_t *>(g.q) + row * g.ldq;
-    const int nv = NV > 0 ? NV : (g.cols + THREADS * 8 - 1) / (THREADS * 8);
+    // f8 activations need no whole row: blockIdx.y takes one block's share of columns
+    const int col0 = OP == kOpAct && FMT == kFmtF8 && NV > 0 ? blockIdx.y * (THREADS * KEEP * 8) : 0;
+    const int nv = FEW ? 1 : NV > 0 ? NV : (g.cols + THREADS * 8 - 1) / (THREADS * 8);
 
-    // norm: h and w; act: gate and up.  `again`: the second reading of a row
-    // that is not kept, by when a + b may have replaced a or b in place.
-    auto fetch = [&](int v, Vec8<T> &a, Vec8<T> &b, bool again) -> int {
-        const int c = (v * THREADS + t) * 8;
-        const int n = g.cols - c;
-        if (n <= 0) {
-            a = Vec8<T>{};
-            b = Vec8<T>{};
-            return n;
+    // Vector v of the row as it lies: norm x, weight and residual; act gate
+    // and up.  `again`: the second reading of a row that is not kept, when
+    // x + residual may have replaced either in place.  Without a branch on
+    // where the row ends, so that a thread's loads are all in flight at once:
+    // a vector that passes the end reads the row's last eight elements, and
+    // settle() moves the ones it owns into place.  (The others may just be
+    // replaced by their sum in place; they are dropped.)
+    auto load = [&](int v, Vec8<T> &a, Vec8<T> &b, Vec8<T> &r, bool again) {
+        const int c = col0 + (v * THREADS + t) * 8;
+        const char *from = again && psum ? psum : pa;
+        if constexpr (FEW) {
+            const int n = t == 0 ? g.cols : 0;
+            load_few(a, from, n);
+            load_few(b, OP == kOpAct ? pb : pw, n);
+            if (OP == kOpNorm && pb) load_few(r, pb, n);
+            return;
         }
+        const int64_t at = static_cast<int64_t>(min(c, g.cols - 8)) * SIZE;
+        load8(a, from + at);
         if constexpr (OP == kOpAct) {
-            a = load8<T>(pa + c, n);
-            b = load8<T>(pb + c, n);
+            load8(b, pb + at);
         } else {
-            b = load8<T>(pw + c, n);
-            if (again && psum) {
-                a = load8<T>(psum + c, n);
-            } else {
-                a = load8<T>(pa + c, n);
-                if (pb) {
-                    const Vec8<T> r = load8<T>(pb + c, n);
+            if (pb && !(again && psum)) load8(r, pb + at);
+            load8(b, pw + at);
+        }
+    };
+    // The vector's own elements in place, zeros past the row; norm: h = x +
+    // residual for x.
+    auto settle = [&](int v, Vec8<T> &a, Vec8<T> &b, const Vec8<T> &r, bool again) {
+        const int c = col0 + (v * THREADS + t) * 8;
+        const int n = g.cols - c;
+        const bool sums = OP == kOpNorm && pb && !(again && psum);
+        if (sums) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) a.e[i] = T::round(T::to_float(a.e[i]) + T::to_float(r.e[i]));
-                }
-                if (psum) store8<T>(psum + c, a, n);
+            for (int i = 0; i < 8; i += 2) T::set2(a.w, i, a.get(i) + r.get(i), a.get(i + 1) + r.get(i + 1));
+        }
+        if (!FEW && n < 8) {
+#pragma unroll 1
+            for (int i = n > 0 ? n : 0; i < 8; ++i) {
+                shift_down(a);
+                shift_down(b);
             }
         }
-        return n;
+        if (sums && psum && n > 0) store8<T>(psum + static_cast<int64_t>(c) * SIZE, a, n);
     };
-    auto values = [&](const Vec8<T> &a, const Vec8<T> &b, float *v) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = value32<OP>(T::to_float(a.e[i]), T::to_float(b.e[i]));
-    };
-    auto value_at = [&](const Vec8<T> &a, const Vec8<T> &b, int i) {
-        return value64<OP>(T::to_float(a.e[i]), T::to_float(b.e[i]));
-    };
+    auto values = [&](const Vec8<T> &a, const Vec8<T> &b, float *v) { values32<T, OP>(a, b, v); };
+    auto value_at = [&](const Vec8<T> &a, const Vec8<T> &b, int i) { return value64<OP>(a.pick(i), b.pick(i)); };
     auto max_at64 = [&](const Vec8<T> &a, const Vec8<T> &b) {
         uint64_t m = 0;
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
             const uint64_t o = abs_bits(value_at(a, b, i));
             m = o > m ? o : m;
         }
         return m;
     };
+    // For each vector of the row: f(v, values, operands), operands(a, b)
+    // giving what the values are made of, for the few that need 64 bits.  The
+    // norm's operands are kept and its products made again; the activation's
+    // values are kept (an exponential each), and its operands too, but for
+    // long s8 rows, which read them again when asked (8192 x 11008: 136 us
+    // with them in registers, 119 without; 8192 x 4096: 40 and 44).
+    constexpr bool KEEP_VALUES = NV > 0 && OP == kOpAct;
+    constexpr bool READ_AGAIN = KEEP_VALUES && FMT == kFmtS8 && NV > 2;
+    Vec8<T> ka[KEEP], kb[KEEP], kr[KEEP];
+    float kv[KEEP_VALUES ? KEEP : 1][8];
+    auto each = [&](auto &&f) {
+        if constexpr (KEEP_VALUES) {
+#pragma unroll
+            for (int v = 0; v < KEEP; ++v)
+                f(v, kv[v], [&](Vec8<T> &a, Vec8<T> &b) {
+                    if constexpr (READ_AGAIN) {
+                        Vec8<T> none;
+                        load(v, a, b, none, true);
+                        settle(v, a, b, none, true);
+                    } else {
+                        a = ka[v];
+                        b = kb[v];
+                    }
+                });
+        } else if constexpr (NV != 0) {
+#pragma unroll
+            for (int v = 0; v < KEEP; ++v) {
+                // hides that the products are those of the first pass, which
+                // the compiler would otherwise keep in registers
+#pragma unroll
+                for (int j = 0; j < Vec8<T>::kWords; ++j) {
+                    uint32_t word = ka[v].w[j];
+                    asm volatile("" : "+v"(word));
+                    ka[v].w[j] = word;
+                }
+                values(ka[v], kb[v], kv[0]);
+                f(v, kv[0], [&](Vec8<T> &a, Vec8<T> &b) {
+                    a = ka[v];
+                    b = kb[v];
+                });
+            }
+        } else {
+            for (int v = 0; v < nv; ++v) {
+                load(v, ka[0], kb[0], kr[0], true);
+                settle(v, ka[0], kb[0], kr[0], true);
+                values(ka[0], kb[0], kv[0]);
+                f(v, kv[0], [&](Vec8<T> &a, Vec8<T> &b) {
+                    a = ka[0];
+                    b = kb[0];
+                });
+            }
+        }
+    };
 
-    Vec8<T> ka[KEEP], kb[KEEP];
+    // Over the row: the sum of squares and the largest |v|.
     double sum = 0.0;
     uint32_t most = 0;
-    auto first = [&](int v, Vec8<T> &a, Vec8<T> &b) {
-        fetch(v, a, b, false);
-        float f[8];
+    auto first = [&](const Vec8<T> &a, const Vec8<T> &b, float *f) {
+        if constexpr (FMT == kFmtS8 || KEEP_VALUES) values(a, b, f);
         if constexpr (FMT == kFmtS8) {
-            values(a, b, f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) most = max(most, abs_bits(f[i]));
         }
         if constexpr (OP == kOpNorm) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const double h = static_cast<double>(T::to_float(a.e[i]));
+                const double h = static_cast<double>(a.get(i));
                 sum = __builtin_fma(h, h, sum);
             }
         }
     };
-    if constexpr (NV > 0) {
+    if constexpr (NV != 0) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) first(v, ka[v], kb[v]);
-    } else {
-        for (int v = 0; v < nv; ++v) first(v, ka[0], kb[0]);
+        for (int v = 0; v < KEEP; ++v) load(v, ka[v], kb[v], kr[v], false);
+#pragma unroll
+        for (int v = 0; v < KEEP; ++v) {
+            settle(v, ka[v], kb[v], kr[v], false);
+            first(ka[v], kb[v], kv[KEEP_VALUES ? v : 0]);
+        }
+    } else if constexpr (OP == kOpNorm || FMT == kFmtS8) {
+        for (int v = 0; v < nv; ++v) {
+            load(v, ka[0], kb[0], kr[0], false);
+            settle(v, ka[0], kb[0], kr[0], false);
+            first(ka[0], kb[0], kv[0]);
+        }
     }
-
-    // Over the row: the sum of squares and the largest |v|.
+    [[maybe_unused]] const uint32_t mine = most;  // this thread's part
     if constexpr (OP == kOpNorm) sum = wave_sum(sum);
     if constexpr (FMT == kFmtS8) most = wave_max(most);
     if constexpr (WAVES > 1 && (OP == kOpNorm || FMT == kFmtS8)) {
@@ -295,19 +467,8 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
             most = max(most, sh_max[w]);
         }
     }
-    const double inv = OP == kOpNorm ? 1.0 / sqrt(sum / g.cols + static_cast<double>(g.eps)) : 1.0;
-
-    // For each vector of the row: f(v, a, b).
-    auto each = [&](auto &&f) {
-        if constexpr (NV > 0) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v) f(v, ka[v], kb[v]);
-        } else {
-            for (int v = 0; v < nv; ++v) {
-                fetch(v, ka[0], kb[0], true);
-                f(v, ka[0], kb[0]);
-            }
-        }
+    auto root = [&]() {
+        return OP == kOpNorm ? 1.0 / sqrt(sum / g.cols + static_cast<double>(g.eps)) : 1.0;
     };
 
     if constexpr (FMT == kFmtS8) {
@@ -316,25 +477,25 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
         // value is off by less than 2^-20), or among all.  Products of 16-bit
         // types are exact in fp32.
         uint64_t m64 = 0;
-        if (plain && OP == kOpNorm && sizeof(Raw) == 2) {
+        if (plain && OP == kOpNorm && SIZE == 2) {
             m64 = abs_bits(static_cast<double>(__uint_as_float(most)));
         } else {
             const uint32_t from = plain ? abs_bits(__uint_as_float(most) * (1.0f - 0x1p-19f)) : 0u;
-            each([&](int, const Vec8<T> &a, const Vec8<T> &b) {
-                if (plain) {
-                    float f[8];
-                    values(a, b, f);
+            if (mine >= from) {
+                each([&](int, const float *f, auto &&operands) {
+                    uint32_t which = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (abs_bits(f[i]) >= from) {
-                            const uint64_t o = abs_bits(value_at(a, b, i));
-                            m64 = o > m64 ? o : m64;
-                        }
-                } else {
-                    const uint64_t o = max_at64(a, b);
-                    m64 = o > m64 ? o : m64;
-                }
-            });
+                    for (int i = 0; i < 8; ++i) which |= abs_bits(f[i]) >= from ? 1u << i : 0u;
+                    if (which == 0) return;
+                    Vec8<T> a, b;
+                    operands(a, b);
+                    for (; which != 0; which &= which - 1) {
+                        const int i = __builtin_ctz(which);
+                        const uint64_t o = abs_bits(value64<OP>(a.pick(i), b.pick(i)));
+                        m64 = o > m64 ? o : m64;
+                    }
+                });
+            }
             m64 = wave_max(m64);
             if constexpr (WAVES > 1) {
                 if ((t & 63) == 0) sh_max64[wave] = m64;
@@ -346,48 +507,76 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
         }
         const double m = __builtin_bit_cast(double, m64);
         const bool number = m64 < kInf64;
-        if (t == 0) g.scale[row] = scale_of(m, inv, 127.0, number);
-        const float k = plain ? static_cast<float>(127.0 / m) : 0.0f;
-        each([&](int v, const Vec8<T> &a, const Vec8<T> &b) {
-            const int c = (v * THREADS + t) * 8;
+        const float k = plain ? 127.0f / static_cast<float>(m) : 0.0f;
+        each([&](int v, const float *f, auto &&operands) {
+            const int c = col0 + (v * THREADS + t) * 8;
             const int n = g.cols - c;
             if (n <= 0) return;
-            int q[8];
+            uint32_t w2[2] = {0, 0};
+            float near = 1.0f;
             if (plain) {
-                float f[8];
-                values(a, b, f);
+                uint32_t y[8];
+                near = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float x = f[i] * k;
-                    const float r = rintf(x);
-                    q[i] = static_cast<int>(r);
-                    if (fabsf(x - r) > 0.5f - kNear)
-                        q[i] = static_cast<int>(rint(value_at(a, b, i) * 127.0 / m));
+                    const float r = __builtin_fmaf(f[i], k, kRound);
+                    y[i] = __float_as_uint(r);
+                    near = fmaxf(near, fabsf(__builtin_fmaf(f[i], k, kRound - r)));
                 }
-            } else {
-                for (int i = 0; i < 8; ++i)
-                    q[i] = number && m64 != 0 ? static_cast<int>(rint(value_at(a, b, i) * 127.0 / m)) : 0;
-            }
-            uint32_t w2[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w2[h] = (q[4 * h] & 0xff) | (q[4 * h + 1] & 0xff) << 8 | (q[4 * h + 2] & 0xff) << 16 |
-                        static_cast<uint32_t>(q[4 * h + 3]) << 24;
-            if (n >= 8) {
-                __builtin_memcpy(pq + c, w2, 8);
-            } else {
-                for (int i = 0; i < n; ++i) pq[c + i] = static_cast<uint8_t>(w2[i >> 2] >> (8 * (i & 3)));
+                for (int h = 0; h < 2; ++h)
+                    w2[h] = __builtin_amdgcn_perm(
+                        __builtin_amdgcn_perm(y[4 * h + 3], y[4 * h + 2], 0x0c0c0400u),
+                        __builtin_amdgcn_perm(y[4 * h + 1], y[4 * h], 0x0c0c0400u), 0x05040100u);
             }
+            if (near > 0.5f - kNear<T, OP>) {
+                Vec8<T> a, b;
+                operands(a, b);
+                uint64_t q = static_cast<uint64_t>(w2[1]) << 32 | w2[0];
+                auto undecided = [&](float x) {
+                    const float r = __builtin_fmaf(x, k, kRound);
+                    return !plain || fabsf(__builtin_fmaf(x, k, kRound - r)) > 0.5f - kNear<T, OP>;
+                };
+                auto decide = [&](int i, float x, float y) {
+                    const int qi = number && m64 != 0 ? static_cast<int>(rint(value64<OP>(x, y) * 127.0 / m)) : 0;
+                    q = (q & ~(0xffull << (8 * i))) | static_cast<uint64_t>(static_cast<uint8_t>(qi)) << (8 * i);
+                };
+                if constexpr (OP == kOpNorm && NV > 2) {
+                    // one index for all lanes and each product made again:
+                    // fewest registers for long rows; short ones take the
+                    // other, faster form (1000 x 2999 fp32: 8.3 and 7.0 us)
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const float x = a.pick(i), y = b.pick(i);
+                        if (undecided(value32<OP>(x, y))) decide(i, x, y);
+                    }
+                } else {
+                    uint32_t which = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) which |= undecided(f[i]) ? 1u << i : 0u;
+                    for (; which != 0; which &= which - 1) {
+                        const int i = __builtin_ctz(which);
+                        decide(i, a.pick(i), b.pick(i));
+                    }
+                }
+                w2[0] = static_cast<uint32_t>(q);
+                w2[1] = static_cast<uint32_t>(q >> 32);
+            }
+            store8_bytes(pq + c, w2[0], w2[1], n);
         });
+        if (t == 0) g.scale[row] = scale_of(m, root(), 127.0, number);
     } else {
-        each([&](int v, const Vec8<T> &a, const Vec8<T> &b) {
-            const int c = (v * THREADS + t) * 8;
+        const double inv = root();
+        each([&](int v, const float *values, auto &&operands) {
+            const int c = col0 + (v * THREADS + t) * 8;
             const int n = g.cols - c;
             float f[8];
-            values(a, b, f);
             uint32_t bits = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) bits = max(bits, abs_bits(f[i]));
+            for (int i = 0; i < 8; ++i) {
+                f[i] = values[i];
+                bits = max(bits, abs_bits(f[i]));
+            }
             bits = block128_max(bits);  // lanes past the row hold zeros
             double m;
             bool number = true;
@@ -399,11 +588,21 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
                 for (int i = 0; i < 8; ++i) f[i] *= k;
             } else {
                 // the 16 lanes of a block come here together
+                Vec8<T> a, b;
+                operands(a, b);
                 const uint64_t m64 = block128_max(max_at64(a, b));
                 m = __builtin_bit_cast(double, m64);
                 number = m64 < kInf64;
-                for (int i = 0; i < 8; ++i)
-                    f[i] = number && m64 != 0 ? static_cast<float>(value_at(a, b, i) * 448.0 / m) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+                if (number && m64 != 0) {
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const float x = static_cast<float>(value_at(a, b, i) * 448.0 / m);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] = i == j ? x : f[j];
+                    }
+                }
             }
             if (n <= 0) return;
             if ((t & 15) == 0) g.scale[row * g.lds + (c >> 7)] = scale_of(m, inv, 448.0, number);
@@ -413,12 +612,7 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
                 w2[h] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h], f[4 * h + 1], 0, false);
                 w2[h] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2], f[4 * h + 3], w2[h], true);
             }
-            if (n >= 8) {
-                __builtin_memcpy(pq + c, w2, 8);
-            } else {
-                for (int i = 0; i < n; ++i)
-                    pq[c + i] = static_cast<uint8_t>(static_cast<uint32_t>(w2[i >> 2]) >> (8 * (i & 3)));
-            }
+            store8_bytes(pq + c, static_cast<uint32_t>(w2[0]), static_cast<uint32_t>(w2[1]), n);
         });
     }
 #endif
