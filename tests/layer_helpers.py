@@ -81,3 +81,81 @@ def check_quantised(q, scale, v, inv, fmt, what, steps=10):
     off = (scale.cpu().double() - want).abs()
     allowed = 2.0 ** -24 * (1 + (steps if fmt == "f8" else 0)) + 2.0 ** -40
     assert (off <= want * allowed).all(), f"{what}: scales off by {(off / want).max()}"
+
+
+# ----- scaled products ---------------------------------------------------------------
+
+def output_tolerance(want, dtype, absolute, relative):
+    """Largest allowed difference from `want` (64 bits): `absolute` plus
+    `relative` of it from the 32-bit arithmetic, then half a step of dtype
+    (none more for float32, whose rounding the arithmetic counts)."""
+    info = torch.finfo(dtype)
+    half = 0.0 if dtype == torch.float32 else info.eps / 2
+    return absolute + want.abs() * ((1 + relative) * (1 + half) - 1) + absolute * half + info.tiny * info.eps / 2
+
+
+def grouped_reference(A, a_scale, B, b_scale, ends, rows, M):
+    """(result in 64 bits, rows that are written) of the grouped product (CPU tensors)."""
+    out = torch.zeros(M, B.shape[1], dtype=torch.float64)
+    written = torch.zeros(M, dtype=torch.bool)
+    T = A.shape[0]
+    for g, (lo, hi) in enumerate(zip(ends, ends[1:])):
+        if hi <= lo:
+            continue
+        idx = rows[lo:hi].long() if rows is not None else torch.arange(lo, hi)
+        inside = (idx >= 0) & (idx < T)
+        safe = torch.where(inside, idx, torch.zeros_like(idx))
+        acc = A[safe].double() @ B[g].double().t()  # exact: below 2^53
+        out[lo:hi] = acc * a_scale[safe].double()[:, None] * b_scale[g].double() * inside[:, None]
+        written[lo:hi] = True
+    return out, written
+
+
+def check_grouped(got, want, written, sentinel, dtype, what):
+    """Rows of the groups within the rounding of an exact sum to fp32, of the
+    scales' product and of their product (2^-24 each; the fourth term covers
+    their squares), then of dtype; other rows untouched."""
+    got = got.cpu()
+    tol = output_tolerance(want[written], dtype, 0.0, 3 * 2.0 ** -24 + 2.0 ** -44)
+    off = (got[written].double() - want[written]).abs()
+    bad = ~(off <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} values off, first at {bad.nonzero()[0].tolist()}, by {off.max()}"
+    rest = got[~written]
+    assert (rest == sentinel).all(), f"{what}: rows outside the groups were written"
+
+
+def f8_reference(A, a_scale, B, b_scale):
+    """(result, the same with every term's magnitude, the same with every
+    term replaced by the largest of its 16 consecutive ones at most), in 64
+    bits, of the block-scaled product (CPU tensors)."""
+    M, K = A.shape
+    N = B.shape[0]
+    a = A.double() * a_scale.double().repeat_interleave(BLOCK, 1)[:, :K]
+    b = B.double() * b_scale.double().repeat_interleave(BLOCK, 0).repeat_interleave(BLOCK, 1)[:N, :K]
+
+    def largest(x):
+        return torch.nn.functional.pad(x.abs(), (0, -K % 16)).view(x.shape[0], -1, 16).amax(2)
+
+    return a @ b.t(), a.abs() @ b.abs().t(), 16 * largest(a) @ largest(b).t()
+
+
+def check_f8(got, reference, K, dtype, what):
+    """Within the error of the sums.
+
+    With `size` the sum of all terms' magnitudes: a block's 128 exact products
+    are added with at most 127 roundings of a step (2^-23, so that truncation
+    is allowed too) each relative to at most its part of `size`; the scales'
+    product and the multiply-add of each of the ceil(K / 128) blocks, and the
+    sum of up to 16 waves' parts, round by 2^-24.  16-bit results: each of 16
+    consecutive products may lose up to 2^-13 of the largest's power of two
+    before."""
+    want, size, pieces = reference
+    got = got.cpu().double()
+    blocks = -(-K // BLOCK)
+    absolute = size * (127 * 2.0 ** -23 + (blocks + 17) * 2.0 ** -24) * (1 + 2.0 ** -10)
+    if dtype != torch.float32:
+        absolute = absolute + pieces * 2.0 ** -13
+    tol = output_tolerance(want, dtype, absolute, 0.0)
+    off = (got - want).abs()
+    bad = ~((off <= tol) | (want.isnan() & got.isnan()))
+    assert not bad.any(), f"{what}: {bad.sum()} values off, first at {bad.nonzero()[0].tolist()}, by {off.max()}"

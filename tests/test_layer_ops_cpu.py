@@ -89,3 +89,79 @@ def test_wrappers_refuse():
         t.swiglu(x, x[:, :128])
     with pytest.raises(ValueError):
         t.rms_norm(x[0], w)
+
+
+# ----- products ----------------------------------------------------------------------
+
+C, BS, RO, OF = (0x100000000 * (i + 1) for i in range(4))
+
+
+def grouped(type=t.BF16, G=4, M=32, N=64, K=128, A=X, lda=128, a_rows=16, a_scale=SC, rows=RO, offsets=OF, B=W,
+            ldb=128, group_b=64 * 128, b_scale=BS, C=C, ldc=64):
+    return t.gemm_s8s8_grouped(type, G, M, N, K, A, lda, a_rows, a_scale, rows, offsets, B, ldb, group_b, b_scale, C,
+                               ldc)
+
+
+def f8(type=t.BF16, M=32, N=200, K=300, A=X, lda=300, a_scale=SC, ldas=3, B=W, ldb=300, b_scale=BS, ldbs=3, C=C,
+       ldc=200):
+    return t.gemm_f8f8_block128(type, M, N, K, A, lda, a_scale, ldas, B, ldb, b_scale, ldbs, C, ldc)
+
+
+def test_grouped_refusals():
+    big = 2 ** 30 + 1
+    for kw in dict(type=3), dict(type=-1), dict(G=-1), dict(M=-1), dict(N=-1), dict(K=-1), dict(lda=127), \
+            dict(ldb=127), dict(ldc=63), dict(a_rows=-1), dict(a_rows=0), dict(K=131072, lda=131072, ldb=131072,
+                                                                              group_b=2 ** 40), \
+            dict(group_b=64 * 128 - 1), dict(group_b=-1), dict(rows=None, a_rows=31), dict(C=C + 1), \
+            dict(type=t.F32, C=C + 2), dict(a_scale=SC + 1), dict(b_scale=BS + 2), dict(rows=RO + 2), \
+            dict(offsets=OF + 1), dict(M=big), dict(N=big, ldc=big), dict(G=big):
+        assert grouped(**kw) == t.ERR_INVALID_VALUE, kw
+    for kw in dict(offsets=None), dict(A=None), dict(B=None), dict(a_scale=None), dict(b_scale=None), dict(C=None):
+        assert grouped(**kw) == t.ERR_NULL_POINTER, kw
+    for kw in dict(C=X), dict(C=W + 3 * 64 * 128), dict(C=SC), dict(C=BS + 4), dict(C=RO), dict(C=OF + 16):
+        assert grouped(**kw) == t.ERR_ALIASING, kw
+    for kw in dict(M=0), dict(N=0), dict(G=0), dict(M=0, A=None, C=None):
+        assert grouped(**kw) == t.OK, kw
+    with pytest.raises(ValueError):
+        grouped(group_b=2 ** 63)
+    with pytest.raises(ValueError):
+        grouped(M=2 ** 32)
+
+
+def test_f8_refusals():
+    big = 2 ** 30 + 1
+    for kw in dict(type=7), dict(M=-1), dict(N=-1), dict(K=-1), dict(lda=299), dict(ldb=299), dict(ldc=199), \
+            dict(ldas=2), dict(ldbs=2), dict(C=C + 1), dict(a_scale=SC + 2), dict(b_scale=BS + 1), \
+            dict(K=big, lda=big, ldb=big, ldas=2 ** 24, ldbs=2 ** 24):
+        assert f8(**kw) == t.ERR_INVALID_VALUE, kw
+    for kw in dict(A=None), dict(B=None), dict(a_scale=None), dict(b_scale=None), dict(C=None):
+        assert f8(**kw) == t.ERR_NULL_POINTER, kw
+    for kw in dict(C=X + 300), dict(C=W), dict(C=SC), dict(C=BS):
+        assert f8(**kw) == t.ERR_ALIASING, kw
+    assert f8(M=0) == t.OK and f8(N=0, ldc=1) == t.OK
+
+
+def test_product_wrappers_refuse():
+    A, s = torch.zeros(4, 256, dtype=torch.int8), torch.zeros(4)
+    B, bs = torch.zeros(3, 8, 256, dtype=torch.int8), torch.zeros(3, 8)
+    off = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        t.grouped_gemm(A, s, B, bs, off)
+    with pytest.raises(TypeError):
+        t.grouped_gemm(A.float(), s, B, bs, off)
+    with pytest.raises(TypeError):
+        t.grouped_gemm(A, s, B.float(), bs, off)
+    for kw in dict(offsets=None), dict(offsets=off[:3]), dict(offsets=off.long()), dict(rows=off.long()), \
+            dict(rows=off[::2]), dict(a_scale=s[:3]), dict(a_scale=s.double()), dict(b_scale=bs[:2]), \
+            dict(b_scale=bs.t().contiguous().t()), dict(B=B[:, :, :255]), dict(B=B.transpose(1, 2)):
+        with pytest.raises(ValueError):
+            t.grouped_gemm(**{**dict(A=A, a_scale=s, B=B, b_scale=bs, offsets=off), **kw})
+    F = torch.zeros(4, 256).to(torch.float8_e4m3fn)
+    fs, gs = torch.zeros(4, 2), torch.zeros(1, 2)
+    with pytest.raises(ValueError, match="GPU"):
+        t.gemm_f8(F, fs, F, gs)
+    with pytest.raises(TypeError):
+        t.gemm_f8(F.view(torch.int8), fs, F, gs)
+    for kw in dict(B=F[:, :128]), dict(a_scale=fs[:3]), dict(b_scale=gs[:, :1]), dict(a_scale=torch.zeros(2, 4).t()):
+        with pytest.raises(ValueError):
+            t.gemm_f8(**{**dict(A=F, a_scale=fs, B=F, b_scale=gs), **kw})

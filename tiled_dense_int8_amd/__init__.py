@@ -92,6 +92,8 @@ _SIGNATURES = {
     "rmsnorm_quant_f8": (_i, [_i] * 3 + [_p, _i, _p, _i, _p, _f, _p, _i, _p, _i, _p, _i, _p]),
     "swiglu_quant_s8": (_i, [_i] * 3 + [_p, _i, _p, _i, _p, _i, _p, _p]),
     "swiglu_quant_f8": (_i, [_i] * 3 + [_p, _i, _p, _i, _p, _i, _p, _i, _p]),
+    "gemm_s8s8_grouped": (_i, [_i] * 5 + [_p, _i, _i, _p, _p, _p, _p, _i, ctypes.c_int64, _p, _p, _i, _p]),
+    "gemm_f8f8_block128": (_i, [_i] * 4 + [_p, _i, _p, _i, _p, _i, _p, _i, _p, _i, _p]),
     "tdi8_status_string": (ctypes.c_char_p, [_i]),
     "tdi8_last_hip_error": (_i, []),
     "tdi8_kernel_code_hash": (ctypes.c_char_p, []),
@@ -488,3 +490,99 @@ def swiglu(gate, up, fmt: str = "s8", out=None, scale=None, stream=None):
     else:
         _call(dev, swiglu_quant_f8, *args, _ld(scale), stream=stream)
     return out, scale
+
+
+# ---- products of 8-bit operands with their scales -------------------------------------
+
+def gemm_s8s8_grouped(type, G, M, N, K, A, lda, a_rows, a_scale, rows, offsets, B, ldb, group_b, b_scale, C, ldc,
+                      stream=0) -> int:
+    _int32(type=type, G=G, M=M, N=N, K=K, lda=lda, a_rows=a_rows, ldb=ldb, ldc=ldc)
+    if not -2 ** 63 <= int(group_b) < 2 ** 63:
+        raise ValueError(f"group_b = {group_b} does not fit the library's 64-bit argument")
+    return _lib.gemm_s8s8_grouped(type, G, M, N, K, A, lda, a_rows, a_scale, rows, offsets, B, ldb, group_b, b_scale,
+                                  C, ldc, stream)
+
+
+def gemm_f8f8_block128(type, M, N, K, A, lda, a_scale, ldas, B, ldb, b_scale, ldbs, C, ldc, stream=0) -> int:
+    _int32(type=type, M=M, N=N, K=K, lda=lda, ldas=ldas, ldb=ldb, ldbs=ldbs, ldc=ldc)
+    return _lib.gemm_f8f8_block128(type, M, N, K, A, lda, a_scale, ldas, B, ldb, b_scale, ldbs, C, ldc, stream)
+
+
+def _vector(name, t, dtype, count) -> None:
+    if t.dtype != dtype or tuple(t.shape) != (count,) or (count > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a dense {dtype} vector of {count} values")
+
+
+def _product_out(M, N, dtype, dev, out, stream):
+    if out is None:
+        if dtype not in _TYPES:
+            raise TypeError("dtype must be float32, bfloat16 or float16")
+        return _empty((M, N), dtype, dev, stream)
+    if out.dtype not in _TYPES:
+        raise TypeError("out must be float32, bfloat16 or float16")
+    _matrix("out", out, out.dtype, (M, N))
+    return out
+
+
+def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtype=torch.bfloat16, stream=None):
+    """int8 products grouped by expert, with their scales: row r of the
+    result, in group g (offsets[g] <= r < offsets[g + 1]), is
+    a_scale[i] * b_scale[g] * (A[i] x B[g] transposed) with i = rows[r] or r.
+
+    A: int8 (T, K); a_scale: float32 (T), as rms_norm and swiglu give them.
+    B: int8 (G, N, K) with b_scale float32 (G, N), or (N, K) with (N).
+    offsets: int32 (G + 1) on the GPU (not needed for one group of all rows).
+    rows: int32 row indices into A, one for each row of the result (rows
+       outside A give zeros); without them the result has A's rows.
+    out: (M, N) of a floating type, or dtype for a new tensor; rows from
+       offsets[G] on are not written.
+    """
+    _matrix("A", A, torch.int8)
+    T, K = A.shape
+    if B.dtype != torch.int8:
+        raise TypeError(f"B must be torch.int8, not {B.dtype}")
+    if B.dim() == 2:
+        B, b_scale = B[None], b_scale[None]
+    if B.dim() != 3 or B.shape[2] != K or (K > 1 and B.stride(2) != 1):
+        raise ValueError("B must be (G, N, K) or (N, K) with A's K and unit stride along it")
+    G, N, _ = B.shape
+    if b_scale.dtype != torch.float32 or tuple(b_scale.shape) != (G, N) or not b_scale.is_contiguous():
+        raise ValueError(f"b_scale must be a dense float32 tensor of shape {(G, N)}")
+    _vector("a_scale", a_scale, torch.float32, T)
+    if offsets is not None:
+        _vector("offsets", offsets, torch.int32, G + 1)
+    elif G != 1:
+        raise ValueError("offsets are needed for more than one group")
+    if rows is not None:
+        _vector("rows", rows, torch.int32, rows.numel())
+    M = T if rows is None else rows.numel()
+    dev = _device_of(*(t for t in (A, a_scale, B, b_scale, offsets, rows, out) if t is not None))
+    out = _product_out(M, N, dtype, dev, out, stream)
+    _call(dev, gemm_s8s8_grouped, _TYPES[out.dtype], G, M, N, K, A.data_ptr(), _ld(A), T, a_scale.data_ptr(),
+          None if rows is None else rows.data_ptr(), None if offsets is None else offsets.data_ptr(), B.data_ptr(),
+          B.stride(1) if N > 1 else max(K, 1), B.stride(0) if G > 1 else 0, b_scale.data_ptr(), out.data_ptr(),
+          _ld(out), stream=stream)
+    return out
+
+
+def gemm_f8(A, a_scale, B, b_scale, out=None, dtype=torch.bfloat16, stream=None):
+    """A x B transposed for e4m3 operands with a scale for each block of 128.
+
+    A: float8_e4m3fn (M, K), a_scale: float32 (M, ceil(K / 128)), as rms_norm
+       and swiglu give them with fmt="f8".
+    B: float8_e4m3fn (N, K), b_scale: float32 (ceil(N / 128), ceil(K / 128)).
+    out: (M, N) of a floating type, or dtype for a new tensor.
+    """
+    _matrix("A", A, torch.float8_e4m3fn)
+    _matrix("B", B, torch.float8_e4m3fn)
+    (M, K), N = A.shape, B.shape[0]
+    if B.shape[1] != K:
+        raise ValueError("inner dimensions differ")
+    kb = -(-K // BLOCK)
+    _matrix("a_scale", a_scale, torch.float32, (M, kb))
+    _matrix("b_scale", b_scale, torch.float32, (-(-N // BLOCK), kb))
+    dev = _device_of(*(t for t in (A, a_scale, B, b_scale, out) if t is not None))
+    out = _product_out(M, N, dtype, dev, out, stream)
+    _call(dev, gemm_f8f8_block128, _TYPES[out.dtype], M, N, K, A.data_ptr(), _ld(A), a_scale.data_ptr(), _ld(a_scale),
+          B.data_ptr(), _ld(B), b_scale.data_ptr(), _ld(b_scale), out.data_ptr(), _ld(out), stream=stream)
+    return out

@@ -148,12 +148,17 @@ def build(jobs: int | None = None, verbose: bool = False, extra_flags: list[str]
                   "-o", os.path.join(bdir, "abi.o")])
     units.append([HIPCC, *flags, "-x", "hip", "-c", os.path.join(CSRC, "selector.cpp"),
                   "-o", os.path.join(bdir, "selector.o")])
-    # the 8-bit layer operators: entry points, and the row kernels by type
+    # the 8-bit layer operators: entry points, the row kernels by type, the
+    # scaled products by operand type
     units.append([HIPCC, *flags, "-x", "hip", "-c", os.path.join(CSRC, "layer_ops.cpp"),
                   "-o", os.path.join(bdir, "layer_ops.o")])
     for ty in ("F32", "Bf16", "F16"):
         units.append([HIPCC, *flags, f"-DTDI8_ROWS_TYPE={ty}", f"-DTDI8_ROWS_REGISTER=register_rows_{ty.lower()}",
                       "-c", os.path.join(CSRC, "quant_rows.hip"), "-o", os.path.join(bdir, f"quant_rows_{ty}.o")])
+    for ty in ("S8", "F8", "F8Wide"):
+        units.append([HIPCC, *flags, f"-DTDI8_PRODUCT_TYPE={ty}",
+                      f"-DTDI8_PRODUCT_REGISTER=register_products_{ty.lower()}",
+                      "-c", os.path.join(CSRC, "stream_product.hip"), "-o", os.path.join(bdir, f"stream_{ty}.o")])
     ceil_obj = os.path.join(bdir, "ceilings.o")
     ceil_unit = [HIPCC, *flags, "-c", os.path.join(CSRC, "ceilings.hip"), "-o", ceil_obj]
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:

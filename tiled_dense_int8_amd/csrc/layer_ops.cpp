@@ -2,7 +2,10 @@
 // the kernel, launch.
 #include <cmath>
 
+#include <climits>
+
 #include "abi_common.h"
+#include "product_table.h"
 #include "quant_rows.h"
 
 namespace tdi8 {
@@ -32,6 +35,8 @@ const RowKernels *row_kernels(int type) {
     return &table[type];
 }
 
+// Sizes stay this far from the end of int, so that a kernel may round one up
+// to its tile.
 constexpr int kMostColumns = 1 << 30;
 constexpr int kBlock = 128;
 
@@ -132,6 +137,83 @@ int act_entry(int fmt, int type, int T, int N, const void *gate, int ldg, const 
     return rows_entry(kOpAct, fmt, type, g, stream);
 }
 
+// e4m3 products with fp32 results have kernels of their own (F8Wide).
+const ProductKernels *product_kernels(bool f8, int type) {
+    static const ProductKernels *table = [] {
+        static ProductKernels k[3];
+        register_products_s8(&k[0]);
+        register_products_f8(&k[1]);
+        register_products_f8wide(&k[2]);
+        return k;
+    }();
+    return &table[!f8 ? 0 : type == TDI8_F32 ? 2 : 1];
+}
+
+// Checks of a scaled product; kb: scales of a row of A (1, or K's blocks of 128).
+int check_product(bool f8, const ProductArgs &g) {
+    const int64_t size = type_bytes(g.type);
+    if (size == 0 || g.M < 0 || g.N < 0 || g.K < 0 || g.G < 0 || g.a_rows < 0 || g.M > kMostColumns ||
+        g.N > kMostColumns || g.K > kMostColumns || g.G > kMostColumns)
+        return TDI8_ERR_INVALID_VALUE;
+    const int64_t kb = (static_cast<int64_t>(g.K) + kBlock - 1) / kBlock;
+    const int64_t kmin = g.K > 1 ? g.K : 1;
+    if (g.lda < kmin || g.ldb < kmin || g.ldc < (g.N > 1 ? g.N : 1)) return TDI8_ERR_INVALID_VALUE;
+    if (f8 && (g.ldas < (kb > 1 ? kb : 1) || g.ldbs < (kb > 1 ? kb : 1))) return TDI8_ERR_INVALID_VALUE;
+    // an int32 sum of K products of int8 cannot wrap
+    if (!f8 && g.K > 131071) return TDI8_ERR_INVALID_VALUE;
+    if (!g.offsets && g.G > 1) return TDI8_ERR_NULL_POINTER;
+    if (!g.rows && g.a_rows < g.M) return TDI8_ERR_INVALID_VALUE;
+    if (g.M == 0 || g.N == 0 || g.G == 0) return TDI8_OK;
+    if (g.a_rows == 0) return TDI8_ERR_INVALID_VALUE;
+    const int64_t b_bytes = (g.N - 1) * g.ldb + g.K;
+    if (g.G > 1 && g.group_b < b_bytes) return TDI8_ERR_INVALID_VALUE;
+    if (!g.C || (!f8 && (!g.a_scale || !g.b_scale))) return TDI8_ERR_NULL_POINTER;
+    if (g.K > 0 && (!g.A || !g.B || !g.a_scale || !g.b_scale)) return TDI8_ERR_NULL_POINTER;
+    if (!aligned(g.C, size) || !aligned(g.a_scale, 4) || !aligned(g.b_scale, 4) || !aligned(g.rows, 4) ||
+        !aligned(g.offsets, 4))
+        return TDI8_ERR_INVALID_VALUE;
+    const int64_t nb = (static_cast<int64_t>(g.N) + kBlock - 1) / kBlock;
+    const Span c = span_of(g.C, g.M, g.N, g.ldc, size);
+    const Span in[6] = {
+        span_of(g.A, g.a_rows, g.K, g.lda, 1),
+        g.K > 0 ? span_of(g.B, g.G, b_bytes, g.group_b, 1) : Span{0, 0},
+        f8 ? span_of(g.a_scale, g.M, kb, g.ldas, 4) : span_of(g.a_scale, 1, g.a_rows, 1, 4),
+        f8 ? span_of(g.b_scale, nb, kb, g.ldbs, 4) : span_of(g.b_scale, g.G, g.N, g.N, 4),
+        span_of(g.rows, 1, g.M, 1, 4),
+        span_of(g.offsets, 1, static_cast<int64_t>(g.G) + 1, 1, 4),
+    };
+    for (const Span &s : in)
+        if (meet(c, s)) return TDI8_ERR_ALIASING;
+    return TDI8_OK;
+}
+
+int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
+    int st = check_product(f8, g);
+    if (st != TDI8_OK) return st;
+    if (g.M == 0 || g.N == 0 || g.G == 0) return TDI8_OK;
+    int units = 0;
+    st = device_units(&units);
+    if (st != TDI8_OK) return st;
+    const bool al = aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 16 == 0 && g.ldb % 16 == 0 && g.K % 16 == 0 &&
+                    (g.G == 1 || g.group_b % 16 == 0);
+    const int64_t rows = g.offsets ? (static_cast<int64_t>(g.M) + g.G - 1) / g.G : g.M;  // of a group, on average
+    const int tile = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
+    const StreamTile t = kStreamTile[tile];
+    // every group that has rows ends in at most one partial tile
+    const int64_t groups = g.G < g.M ? g.G : g.M;
+    const int64_t tm = (g.M + groups * (t.bm - 1)) / t.bm;
+    const int64_t tn = (static_cast<int64_t>(g.N) + t.bn - 1) / t.bn;
+    const int64_t threads = 64 * t.waves;
+    if (tm > INT_MAX || tm * tn > INT_MAX / threads - 8) return TDI8_ERR_INVALID_VALUE;
+    g.tiles_m = static_cast<int>(tm);
+    g.tiles_n = static_cast<int>(tn);
+    const unsigned blocks = static_cast<unsigned>((tm * tn + 7) / 8 * 8);
+    void *args[] = {&g};
+    const hipError_t e = hipLaunchKernel(product_kernels(f8, g.type)->stream[tile][al ? 1 : 0], dim3(blocks),
+                                         dim3(static_cast<unsigned>(threads)), args, 0, stream);
+    return e == hipSuccess ? TDI8_OK : hip_fail(e);
+}
+
 }  // namespace
 }  // namespace tdi8
 
@@ -160,6 +242,53 @@ int swiglu_quant_s8(int type, int T, int N, const void *gate, int ldg, const voi
 int swiglu_quant_f8(int type, int T, int N, const void *gate, int ldg, const void *up, int ldu, uint8_t *q,
                     int ldq, float *scale, int lds, hipStream_t stream) {
     return act_entry(kFmtF8, type, T, N, gate, ldg, up, ldu, q, ldq, scale, lds, stream);
+}
+
+int gemm_s8s8_grouped(int type, int G, int M, int N, int K, const int8_t *A, int lda, int a_rows,
+                      const float *a_scale, const int32_t *rows, const int32_t *offsets, const int8_t *B, int ldb,
+                      int64_t group_b, const float *b_scale, void *C, int ldc, hipStream_t stream) {
+    ProductArgs g{};
+    g.A = A;
+    g.B = B;
+    g.C = C;
+    g.a_scale = a_scale;
+    g.b_scale = b_scale;
+    g.rows = rows;
+    g.offsets = offsets;
+    g.lda = lda;
+    g.ldb = ldb;
+    g.ldc = ldc;
+    g.group_b = group_b;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.G = G;
+    g.a_rows = a_rows;
+    g.type = type;
+    return product_entry(false, g, stream);
+}
+
+int gemm_f8f8_block128(int type, int M, int N, int K, const uint8_t *A, int lda, const float *a_scale, int ldas,
+                       const uint8_t *B, int ldb, const float *b_scale, int ldbs, void *C, int ldc,
+                       hipStream_t stream) {
+    ProductArgs g{};
+    g.A = reinterpret_cast<const int8_t *>(A);
+    g.B = reinterpret_cast<const int8_t *>(B);
+    g.C = C;
+    g.a_scale = a_scale;
+    g.b_scale = b_scale;
+    g.lda = lda;
+    g.ldb = ldb;
+    g.ldc = ldc;
+    g.ldas = ldas;
+    g.ldbs = ldbs;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.G = 1;
+    g.a_rows = M;
+    g.type = type;
+    return product_entry(true, g, stream);
 }
 
 }  // extern "C"

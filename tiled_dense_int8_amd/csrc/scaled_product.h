@@ -1,0 +1,132 @@
+// Products of 8-bit operands with their scales: int8 grouped by expert and
+// e4m3 with a scale for each block of 128.  Arguments, the search for a
+// block's rows, and the rounded store that the kernels share.
+#pragma once
+
+#include "device_common.h"
+
+namespace tdi8 {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+struct ProductArgs {
+    const int8_t *A, *B;  // int8 or e4m3 bytes, K contiguous
+    void *C;
+    const float *a_scale, *b_scale;
+    const int32_t *rows;     // A's row of each C row, or null: its own
+    const int32_t *offsets;  // G + 1 ends of the groups' rows, or null: one group of all
+    int64_t lda, ldb, ldc;
+    int64_t group_b;         // bytes from one group's B to the next
+    int64_t ldas, ldbs;      // e4m3: leading dimensions of the scales
+    int M, N, K, G;          // M: rows of C
+    int a_rows;              // rows of A (entries of `rows` outside give rows of zeros)
+    int type;                // tdi8_type of C
+    int tiles_m, tiles_n;    // tiles of the grid: tiles_m bounds the groups' row tiles
+};
+
+// The rows [m0, m0 + BM) within one group, as far as `end`.
+struct RowTile {
+    int group, m0, end;
+};
+
+// Row tile `tile` of the groups' tiles in order (ceil(rows / BM) for each
+// group), and how many there are.  Every wave searches by itself: 64 offsets a
+// step, a prefix sum over the lanes.  Offsets are clamped to [0, M] and to
+// rising order, so that no value of theirs leads outside C.
+__device__ __forceinline__ bool find_rows(const ProductArgs &g, int bm, int tile, RowTile &out, int *count) {
+    if (!g.offsets) {
+        const int tiles = (g.M + bm - 1) / bm;
+        if (count) *count = tiles;
+        out = {0, tile * bm, g.M};
+        return tile < tiles;
+    }
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    bool found = false;
+    for (int base = 0; base < g.G; base += 64) {
+        const int e = base + lane;
+        int lo = 0, hi = 0;
+        if (e < g.G) {
+            lo = min(max(g.offsets[e], 0), g.M);
+            hi = min(max(g.offsets[e + 1], lo), g.M);
+        }
+        const int tiles = (hi - lo + bm - 1) / bm;
+        int sum = tiles;
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const int o = __shfl_up(sum, s);
+            if (lane >= s) sum += o;
+        }
+        const int total = __builtin_amdgcn_readlane(sum, 63);
+        if (!found && tile - before < total) {
+            const int l = __builtin_ctzll(__ballot(before + sum > tile));
+            const int first = before + __builtin_amdgcn_readlane(sum - tiles, l);
+            out.group = base + l;
+            out.m0 = __builtin_amdgcn_readlane(lo, l) + (tile - first) * bm;
+            out.end = __builtin_amdgcn_readlane(hi, l);
+            found = true;
+            if (!count) return true;
+        }
+        before += total;
+    }
+    if (count) *count = before;
+    return found;
+}
+
+// Position of block `bid` among `total` that are dealt out so that each XCD
+// (blocks go to the 8 XCDs in turn) takes one run of consecutive positions;
+// total or more if it has none.  Launched in multiples of 8.
+__device__ __forceinline__ int64_t xcd_run(int64_t bid, int64_t total) {
+    const int64_t per = (total + 7) >> 3;
+    const int64_t at = bid >> 3;
+    return at < per ? (bid & 7) * per + at : total;
+}
+
+// A's row of C row m: its own or rows[m], or -1 for an entry outside A.
+__device__ __forceinline__ int a_row(const ProductArgs &g, int m) {
+    const int r = g.rows ? g.rows[m] : m;
+    return static_cast<unsigned>(r) < static_cast<unsigned>(g.a_rows) ? r : -1;
+}
+
+// Four consecutive values of row m from column n on, rounded to C's type
+// (once, to nearest even); columns past N are left out.
+__device__ __forceinline__ void store_row4(const ProductArgs &g, int64_t m, int n, f32x4 v) {
+    const int64_t at = m * g.ldc + n;
+    const int left = g.N - n;
+    if (g.type == 0) {
+        float *p = static_cast<float *>(g.C) + at;
+        if (left >= 4) {
+            __builtin_memcpy(p, &v, 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (e < left) p[e] = v[e];
+        }
+        return;
+    }
+    uint32_t w[2];
+    if (g.type == 1) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 a = {static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1])};
+        const bf16x2 b = {static_cast<__bf16>(v[2]), static_cast<__bf16>(v[3])};
+        w[0] = __builtin_bit_cast(uint32_t, a);
+        w[1] = __builtin_bit_cast(uint32_t, b);
+    } else {
+        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+        const f16x2 a = {static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1])};
+        const f16x2 b = {static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])};
+        w[0] = __builtin_bit_cast(uint32_t, a);
+        w[1] = __builtin_bit_cast(uint32_t, b);
+    }
+    uint16_t *p = static_cast<uint16_t *>(g.C) + at;
+    if (left >= 4) {
+        __builtin_memcpy(p, w, 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) p[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
+}  // namespace tdi8
