@@ -8,6 +8,11 @@
 #include "product_table.h"
 #include "quant_rows.h"
 
+#ifndef STREAM_ROWS
+#define STREAM_ROWS 32
+#define T128 96
+#define T256 192
+#endif
 namespace tdi8 {
 namespace {
 
@@ -149,6 +154,15 @@ const ProductKernels *product_kernels(bool f8, int type) {
     return &table[!f8 ? 0 : type == TDI8_F32 ? 2 : 1];
 }
 
+const void *const *grouped_tiles() {
+    static const void *const *table = [] {
+        static const void *k[kLdsTiles];
+        register_grouped_tiles(k);
+        return k;
+    }();
+    return table;
+}
+
 // Checks of a scaled product; kb: scales of a row of A (1, or K's blocks of 128).
 int check_product(bool f8, const ProductArgs &g) {
     const int64_t size = type_bytes(g.type);
@@ -197,20 +211,33 @@ int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
     const bool al = aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 16 == 0 && g.ldb % 16 == 0 && g.K % 16 == 0 &&
                     (g.G == 1 || g.group_b % 16 == 0);
     const int64_t rows = g.offsets ? (static_cast<int64_t>(g.M) + g.G - 1) / g.G : g.M;  // of a group, on average
-    const int tile = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
-    const StreamTile t = kStreamTile[tile];
+    const void *kernel;
+    int bm, bn, threads;
+    if (!f8 && al && rows > STREAM_ROWS) {
+        const int tile = rows > T256 ? 2 : rows > T128 ? 1 : 0;
+        const LdsTile t = kGroupedTile[tile];
+        kernel = grouped_tiles()[tile];
+        bm = t.bm;
+        bn = t.bn;
+        threads = t.threads;
+    } else {
+        const int tile = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
+        const StreamTile t = kStreamTile[tile];
+        kernel = product_kernels(f8, g.type)->stream[tile][al ? 1 : 0];
+        bm = t.bm;
+        bn = t.bn;
+        threads = 64 * t.waves;
+    }
     // every group that has rows ends in at most one partial tile
     const int64_t groups = g.G < g.M ? g.G : g.M;
-    const int64_t tm = (g.M + groups * (t.bm - 1)) / t.bm;
-    const int64_t tn = (static_cast<int64_t>(g.N) + t.bn - 1) / t.bn;
-    const int64_t threads = 64 * t.waves;
+    const int64_t tm = (g.M + groups * (bm - 1)) / bm;
+    const int64_t tn = (static_cast<int64_t>(g.N) + bn - 1) / bn;
     if (tm > INT_MAX || tm * tn > INT_MAX / threads - 8) return TDI8_ERR_INVALID_VALUE;
     g.tiles_m = static_cast<int>(tm);
     g.tiles_n = static_cast<int>(tn);
     const unsigned blocks = static_cast<unsigned>((tm * tn + 7) / 8 * 8);
     void *args[] = {&g};
-    const hipError_t e = hipLaunchKernel(product_kernels(f8, g.type)->stream[tile][al ? 1 : 0], dim3(blocks),
-                                         dim3(static_cast<unsigned>(threads)), args, 0, stream);
+    const hipError_t e = hipLaunchKernel(kernel, dim3(blocks), dim3(static_cast<unsigned>(threads)), args, 0, stream);
     return e == hipSuccess ? TDI8_OK : hip_fail(e);
 }
 

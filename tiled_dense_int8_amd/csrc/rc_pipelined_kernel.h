@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "scaled_product.h"
 #include "tiled_kernel.h"
 
 namespace tdi8 {
@@ -83,10 +84,15 @@ constexpr int step_group(int ks, int f) {
 // tile leaves straight from the accumulation registers (no LDS pass, no
 // barrier), so its stores drain while the matrix work of the next tile
 // runs.  Whole tiles only (M, N and K multiples of the tile), GEMM source.
+// SRC: 0 the product, 1 the convolution, 2 the product grouped by expert: the
+// rows of one group (g.M its end, at: where the tile lies), A's rows gathered
+// through an index, C scaled and rounded (pr: its arguments).
 template <int MF, int WM, int WN, int MT, int NT, int BK, int STAGES, bool BROW, bool SPLIT, bool EDGE, int SRC,
           bool PERSIST = false>
-__device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvParams &cv, int nblocks = 1) {
-    static_assert(SRC == 0 || (!BROW && !SPLIT), "the convolution source is column-major B, unsplit");
+__device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvParams &cv, int nblocks = 1,
+                                               const ProductArgs *pr = nullptr, RowTile at = {0, 0, 0}, int at_n = 0) {
+    static_assert(SRC == 0 || (!BROW && !SPLIT), "the other sources are column-major B, unsplit");
+    static_assert(SRC != 2 || (EDGE && MF == 32), "the grouped source: groups end inside tiles");
     static_assert(!PERSIST || (SRC == 0 && !SPLIT && !EDGE && MF == 32), "persistent form: whole tiles, GEMM");
     constexpr int NW = WM * WN;
     constexpr int BM = WM * MF * MT;
@@ -115,7 +121,12 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
     using Acc = typename Mfma<MF>::Acc;
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
 
-    __shared__ __attribute__((aligned(1024))) int8_t lds[STAGES * STAGE];
+    // (grouped: the rows' scales behind the stages, in the same array: with a
+    // second one the compiler waits for every DMA load before an operand read,
+    // 71 -> 89 us where 64 groups have a row each)
+    __shared__ __attribute__((aligned(1024))) int8_t lds[STAGES * STAGE + (SRC == 2 ? 8 * BM : 0)];
+    [[maybe_unused]] float *row_scale = reinterpret_cast<float *>(lds + STAGES * STAGE);
+    [[maybe_unused]] int *row_in = reinterpret_cast<int *>(lds + STAGES * STAGE + 4 * BM);
     BlockStamp stamp;
     stamp.begin();
 
@@ -142,14 +153,14 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
             k_begin = static_cast<int64_t>(slice) * kslice;
         }
     }
-    int tm, tn;
-    tile_of_block(g, bid, tm, tn);
-    const int m0 = tm * BM;
-    const int n0 = tn * BN;
+    int tm = 0, tn = 0;
+    if constexpr (SRC != 2) tile_of_block(g, bid, tm, tn);
+    const int m0 = SRC == 2 ? at.m0 : tm * BM;
+    const int n0 = SRC == 2 ? at_n : tn * BN;
     // GEMM: K is a multiple of 16 (of BK without EDGE); a last partial K tile
     // is completed with zero chunks.  Convolution: the reduction R*S*C is a
     // multiple of 16, completed the same way.
-    const int nk = SRC == 0 ? (kslice + BK - 1) / BK : (cv.rsc + BK - 1) / BK;
+    const int nk = SRC != 1 ? (kslice + BK - 1) / BK : (cv.rsc + BK - 1) / BK;
 
     // Per-lane source pointers of this wave's load instructions (K offset 0).
     // GEMM: chunks outside the operands read the zero chunk: A rows past M,
@@ -195,6 +206,12 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
         if (q < A_CHUNKS) {
             const int r = q / CPR;
             const int c = (q % CPR) ^ chunk_swizzle<CPR>(r);
+            if constexpr (SRC == 2) {
+                const int row = m0 + r < g.M ? a_row(*pr, m0 + r) : -1;
+                klim[i] = row >= 0 ? kslice - 16 * c : 0;
+                src[i] = g.A + static_cast<int64_t>(row >= 0 ? row : 0) * g.lda + 16 * c;
+                continue;
+            }
             const bool ok = !EDGE || m0 + r < g.M;
             klim[i] = ok ? kslice - 16 * c : 0;
             src[i] = g.A + static_cast<int64_t>(ok ? m0 + r : m0) * g.lda + k_begin + 16 * c;
@@ -232,7 +249,7 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
         if constexpr (PERSIST) {
             const bool is_a = i < A_CHUNKS / 64 / NW;
             return src[i] + (is_a ? la : lb) + koff(i, lt);
-        } else if constexpr (SRC == 0 && EDGE) {
+        } else if constexpr (SRC != 1 && EDGE) {
             return kt * BK < klim[i] ? src[i] + koff(i, kt) : zero_chunk;
         } else if constexpr (SRC == 0) {
             return src[i] + koff(i, kt);
@@ -652,6 +669,21 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
         constexpr int RP = RP0 < BM ? RP0 : BM;
         static_assert(RP >= MF, "stage buffers hold at least one instruction tile of rows");
         int32_t *cl = reinterpret_cast<int32_t *>(lds);
+        // Grouped: the scales of the tile's rows, and of the four columns that
+        // this thread stores in every pass.
+        [[maybe_unused]] f32x4 col_scale = {0, 0, 0, 0};
+        if constexpr (SRC == 2) {
+            static_assert(NW * 64 % (BN / 4) == 0, "a thread keeps its columns");
+            for (int r = threadIdx.x; r < BM; r += NW * 64) {
+                const int row = m0 + r < g.M ? a_row(*pr, m0 + r) : -1;
+                row_in[r] = row >= 0;
+                row_scale[r] = row >= 0 ? pr->a_scale[row] : 0.0f;
+            }
+            const float *sb = pr->b_scale + static_cast<int64_t>(at.group) * g.N;
+            const int n = n0 + 4 * static_cast<int>(threadIdx.x % (BN / 4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) col_scale[e] = sb[min(n + e, g.N - 1)];
+        }
         for (int p0 = 0; p0 < BM; p0 += RP) {
             __syncthreads();
 #pragma unroll
@@ -676,6 +708,17 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
                 const int r = idx / (BN / 4);
                 const int c4 = idx - r * (BN / 4);
                 const i32x4 v = *reinterpret_cast<const i32x4 *>(cl + r * RS + 4 * c4);
+                if constexpr (SRC == 2) {
+                    const int m = m0 + p0 + r;
+                    if (m < g.M && n0 + 4 * c4 < g.N) {
+                        f32x4 f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            f[e] = row_in[p0 + r] ? static_cast<float>(v[e]) * (row_scale[p0 + r] * col_scale[e]) : 0.0f;
+                        store_row4<true>(*pr, m, n0 + 4 * c4, f);
+                    }
+                    continue;
+                }
                 if (SRC == 0 && full_rows)
                     store4_nt<true>(g, m0 + p0 + r, n0 + 4 * c4, v);
                 else
@@ -725,6 +768,35 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_rc_persistent_kernel(GemmAr
 template <int MF, int WM, int WN, int MT, int NT, int BK, int STAGES>
 __global__ void __launch_bounds__(WM * WN * 64) conv_implicit_kernel(GemmArgs g, ConvParams cv) {
     pipelined_body<MF, WM, WN, MT, NT, BK, STAGES, false, false, true, 1>(g, cv);
+}
+
+// Products grouped by expert: the blocks of one XCD take consecutive
+// positions of the order below, four row tiles of the groups' list by all
+// column tiles (as tile_of_block), so they share A and B rows in its L2.
+template <int MF, int WM, int WN, int MT, int NT, int BK, int STAGES>
+__global__ void __launch_bounds__(WM * WN * 64) grouped_pipelined_kernel(ProductArgs p) {
+    constexpr int BM = WM * MF * MT, BN = WN * MF * NT;
+    RowTile rt{0, 0, 0};
+    int tiles = 0;
+    find_rows(p, BM, -1, rt, &tiles);
+    const int64_t total = static_cast<int64_t>(tiles) * p.tiles_n;
+    const int64_t l = xcd_run(blockIdx.x, total);
+    if (l >= total) return;
+    const int64_t gsize = 4ll * p.tiles_n;
+    const int first = static_cast<int>(l / gsize) * 4;
+    const int rows = min(tiles - first, 4);
+    const int within = static_cast<int>(l % gsize);
+    if (!find_rows(p, BM, first + within % rows, rt, nullptr)) return;
+    GemmArgs g{};
+    g.A = p.A;
+    g.B = p.B + rt.group * p.group_b;
+    g.lda = p.lda;
+    g.ldb = p.ldb;
+    g.M = rt.end;
+    g.N = p.N;
+    g.K = p.K;
+    pipelined_body<MF, WM, WN, MT, NT, BK, STAGES, false, false, true, 2>(g, ConvParams{}, 1, &p, rt,
+                                                                          within / rows * BN);
 }
 
 }  // namespace tdi8

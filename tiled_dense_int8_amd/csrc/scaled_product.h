@@ -90,14 +90,20 @@ __device__ __forceinline__ int a_row(const ProductArgs &g, int m) {
 }
 
 // Four consecutive values of row m from column n on, rounded to C's type
-// (once, to nearest even); columns past N are left out.
+// (once, to nearest even); columns past N are left out.  STREAM: with the
+// non-temporal hint, where a wave's stores cover whole lines.
+template <bool STREAM = false>
 __device__ __forceinline__ void store_row4(const ProductArgs &g, int64_t m, int n, f32x4 v) {
     const int64_t at = m * g.ldc + n;
     const int left = g.N - n;
     if (g.type == 0) {
         float *p = static_cast<float *>(g.C) + at;
+        typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
         if (left >= 4) {
-            __builtin_memcpy(p, &v, 16);
+            if (STREAM)
+                __builtin_nontemporal_store(v, reinterpret_cast<f32x4_a4 *>(p));
+            else
+                __builtin_memcpy(p, &v, 16);
         } else {
 #pragma unroll
             for (int e = 0; e < 3; ++e)
@@ -120,13 +126,31 @@ __device__ __forceinline__ void store_row4(const ProductArgs &g, int64_t m, int 
         w[1] = __builtin_bit_cast(uint32_t, b);
     }
     uint16_t *p = static_cast<uint16_t *>(g.C) + at;
+    typedef uint32_t u32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
     if (left >= 4) {
-        __builtin_memcpy(p, w, 8);
+        // (at 2-byte alignment the hinted store would be split)
+        if (STREAM && (reinterpret_cast<uintptr_t>(p) & 3) == 0)
+            __builtin_nontemporal_store(u32x2_a4{w[0], w[1]}, reinterpret_cast<u32x2_a4 *>(p));
+        else
+            __builtin_memcpy(p, w, 8);
     } else {
 #pragma unroll
         for (int e = 0; e < 3; ++e)
             if (e < left) p[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
     }
+}
+
+// Four sums of int8 products of row m (below `end`) from column n on, scaled.
+__device__ __forceinline__ void store_scaled4(const ProductArgs &g, int group, int end, int m, int n, i32x4 sum) {
+    if (m >= end || n >= g.N) return;
+    const int row = a_row(g, m);
+    const float sa = row < 0 ? 0.0f : g.a_scale[row];
+    const float *sb = g.b_scale + static_cast<int64_t>(group) * g.N;
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        v[e] = row < 0 ? 0.0f : static_cast<float>(sum[e]) * (sa * sb[min(n + e, g.N - 1)]);
+    store_row4(g, m, n, v);
 }
 
 }  // namespace tdi8

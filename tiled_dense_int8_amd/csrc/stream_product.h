@@ -168,18 +168,10 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
         Acc sum = part[r * RS / 4 + c];
 #pragma unroll
         for (int w = 1; w < W; ++w) sum += part[(w * BM + r) * RS / 4 + c];
-        f32x4 v;
-        if constexpr (E::kBlockScales) {
-            v = sum;
-        } else {
-            const int row = a_row(g, m);
-            const float sa = row < 0 ? 0.0f : g.a_scale[row];
-            const float *sb = g.b_scale + static_cast<int64_t>(rt.group) * g.N;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = row < 0 ? 0.0f : static_cast<float>(sum[e]) * (sa * sb[min(n + e, g.N - 1)]);
-        }
-        store_row4(g, m, n, v);
+        if constexpr (E::kBlockScales)
+            store_row4(g, m, n, sum);
+        else
+            store_scaled4(g, rt.group, rt.end, m, n, sum);
     }
 #endif
 }
