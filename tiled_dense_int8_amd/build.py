@@ -159,7 +159,7 @@ def build(jobs: int | None = None, verbose: bool = False, extra_flags: list[str]
         units.append([HIPCC, *flags, f"-DTDI8_PRODUCT_TYPE={ty}",
                       f"-DTDI8_PRODUCT_REGISTER=register_products_{ty.lower()}",
                       "-c", os.path.join(CSRC, "stream_product.hip"), "-o", os.path.join(bdir, f"stream_{ty}.o")])
-    for name in ("grouped_tiles",):
+    for name in ("grouped_tiles", "block_scale_tiles"):
         units.append([HIPCC, *flags, "-c", os.path.join(CSRC, name + ".hip"), "-o", os.path.join(bdir, name + ".o")])
     ceil_obj = os.path.join(bdir, "ceilings.o")
     ceil_unit = [HIPCC, *flags, "-c", os.path.join(CSRC, "ceilings.hip"), "-o", ceil_obj]

@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include <climits>
+#include <cstdlib>
 
 #include "abi_common.h"
 #include "product_table.h"
@@ -154,13 +155,20 @@ const ProductKernels *product_kernels(bool f8, int type) {
     return &table[!f8 ? 0 : type == TDI8_F32 ? 2 : 1];
 }
 
-const void *const *grouped_tiles() {
-    static const void *const *table = [] {
-        static const void *k[kLdsTiles];
-        register_grouped_tiles(k);
-        return k;
+// LDS tile kernels of an operand type, and their tiles.
+struct TileSet {
+    const void *kernel[kLdsTiles];
+    const LdsTile *tile;
+};
+const TileSet &tile_set(bool f8, int type) {
+    static const TileSet *table = [] {
+        static TileSet t[3] = {{{}, kGroupedTile}, {{}, kF8Tile}, {{}, kF8WideTile}};
+        register_grouped_tiles(t[0].kernel);
+        register_f8_tiles(t[1].kernel);
+        register_f8wide_tiles(t[2].kernel);
+        return t;
     }();
-    return table;
+    return table[!f8 ? 0 : type == TDI8_F32 ? 2 : 1];
 }
 
 // Checks of a scaled product; kb: scales of a row of A (1, or K's blocks of 128).
@@ -213,15 +221,21 @@ int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
     const int64_t rows = g.offsets ? (static_cast<int64_t>(g.M) + g.G - 1) / g.G : g.M;  // of a group, on average
     const void *kernel;
     int bm, bn, threads;
-    if (!f8 && al && rows > STREAM_ROWS) {
+    // e4m3 tiles address their operands by 32-bit offsets
+    const bool near = !f8 || (256 * (g.lda > g.ldb ? g.lda : g.ldb) + g.K < INT_MAX && 256 * 4 * g.ldas + 4 * g.K < INT_MAX);
+    if (al && near && rows > STREAM_ROWS) {
         const int tile = rows > T256 ? 2 : rows > T128 ? 1 : 0;
-        const LdsTile t = kGroupedTile[tile];
-        kernel = grouped_tiles()[tile];
+        const LdsTile t = tile_set(f8, g.type).tile[tile];
+        kernel = tile_set(f8, g.type).kernel[tile];
         bm = t.bm;
         bn = t.bn;
         threads = t.threads;
     } else {
+#ifdef MANY
+        static const int tile = atoi(getenv("STILE"));
+#else
         const int tile = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
+#endif
         const StreamTile t = kStreamTile[tile];
         kernel = product_kernels(f8, g.type)->stream[tile][al ? 1 : 0];
         bm = t.bm;

@@ -157,6 +157,8 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
     if constexpr (SRC != 2) tile_of_block(g, bid, tm, tn);
     const int m0 = SRC == 2 ? at.m0 : tm * BM;
     const int n0 = SRC == 2 ? at_n : tn * BN;
+    [[maybe_unused]] const bool idle =
+        SRC == 2 && m0 + __builtin_amdgcn_readfirstlane(wm) * (MT * MF) >= g.M;
     // GEMM: K is a multiple of 16 (of BK without EDGE); a last partial K tile
     // is completed with zero chunks.  Convolution: the reduction R*S*C is a
     // multiple of 16, completed the same way.
@@ -411,6 +413,22 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
         constexpr bool LOAD = decltype(load_tag)::value;
         constexpr bool NEXT = decltype(next_tag)::value;
         constexpr bool WAITN = decltype(waitn_tag)::value;
+        if constexpr (SRC == 2) {
+            // A wave whose rows all lie past the group's end keeps up the
+            // loads and the barrier and leaves its matrix cores to the others.
+            if (idle) {
+                if constexpr (NEXT) {
+                    if constexpr (WAITN) {
+                        TDI8_WAIT_VMCNT((STAGES - 2) * LPW);
+                    } else {
+                        TDI8_WAIT_VMCNT(0);
+                    }
+                    block_barrier();
+                }
+                if constexpr (LOAD) issue(t + STAGES);
+                return;
+            }
+        }
 #pragma unroll
         for (int gi = 0; gi < KG; ++gi) {
             const int cur = gi & 1;

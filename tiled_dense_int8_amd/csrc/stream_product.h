@@ -83,7 +83,7 @@ struct F8Wide {
 constexpr int kChunk = 128;
 
 // ALIGNED: A, B, lda, ldb, group_b and K are multiples of 16.
-template <class E, int MT, int NT, int W, bool ALIGNED>
+template <class E, int MT, int NT, int W, int U, bool ALIGNED>
 __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int BM = 16 * MT, BN = 16 * NT;
@@ -129,30 +129,49 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
         else
             return load16_masked(p + k, clamp16(g.K - k));
     };
-    auto chunk = [&](int kc, auto whole) {
-        const int k = kc * kChunk + 16 * q;
-        i32x4 a[MT][2], b[NT][2];
-        float s[MT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            b[j][0] = load(pb[j], k, whole);
-            b[j][1] = load(pb[j], k + 64, whole);
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            a[i][0] = load(pa[i], k, whole);
-            a[i][1] = load(pa[i], k + 64, whole);
-            s[i] = E::kBlockScales ? psa[i][kc] * psb[kc] : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) E::chunk(a[i], b[j], s[i], acc[i][j]);
-    };
     const int whole = g.K / kChunk;
-#pragma unroll 4
-    for (int kc = wave; kc < whole; kc += W) chunk(kc, std::true_type{});
-    if (whole * kChunk < g.K && whole % W == wave) chunk(whole, std::false_type{});
+#ifdef ROT
+    const int first = whole > 0 ? tn ROT % whole : 0;
+    auto turn = [&](int c) { c += first; return c >= whole && c - first < whole ? c - whole : c - (c - first >= whole ? first : 0); };
+#else
+    auto turn = [&](int c) { return c; };
+#endif
+    // U chunks a time, all of their loads before the first product: a wave has
+    // U (MT + NT) KiB on the way at once.
+    auto chunks = [&](int kc, auto count, auto whole) {
+        constexpr int C = decltype(count)::value;
+        i32x4 a[C][MT][2], b[C][NT][2];
+        float s[C][MT];
+#pragma unroll
+        for (int u = 0; u < C; ++u) {
+            const int ck = turn(kc + u * W);
+            const int k = ck * kChunk + 16 * q;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                b[u][j][0] = load(pb[j], k, whole);
+                b[u][j][1] = load(pb[j], k + 64, whole);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                a[u][i][0] = load(pa[i], k, whole);
+                a[u][i][1] = load(pa[i], k + 64, whole);
+                s[u][i] = E::kBlockScales ? psa[i][ck] * psb[ck] : 0.0f;
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) E::chunk(a[u][i], b[u][j], s[u][i], acc[i][j]);
+    };
+    using One = std::integral_constant<int, 1>;
+    int kc = wave;
+    if constexpr (U > 1)
+        for (; kc + (U - 1) * W < whole; kc += U * W) chunks(kc, std::integral_constant<int, U>{}, std::true_type{});
+    for (; kc < whole; kc += W) chunks(kc, One{}, std::true_type{});
+    if (whole * kChunk < g.K && whole % W == wave) chunks(whole, One{}, std::false_type{});
 
     // partial tiles: a lane writes four consecutive columns of its row
 #pragma unroll

@@ -13,9 +13,9 @@ template <int T>
 static void register_stream(ProductKernels *k) {
     constexpr StreamTile t = kStreamTile[T];
     k->stream[T][0] = reinterpret_cast<const void *>(
-        &stream_product_kernel<TDI8_PRODUCT_TYPE, t.bm / 16, t.bn / 16, t.waves, false>);
+        &stream_product_kernel<TDI8_PRODUCT_TYPE, t.bm / 16, t.bn / 16, t.waves, t.batch, false>);
     k->stream[T][1] = reinterpret_cast<const void *>(
-        &stream_product_kernel<TDI8_PRODUCT_TYPE, t.bm / 16, t.bn / 16, t.waves, true>);
+        &stream_product_kernel<TDI8_PRODUCT_TYPE, t.bm / 16, t.bn / 16, t.waves, t.batch, true>);
     if constexpr (T + 1 < kStreamTiles) register_stream<T + 1>(k);
 }
 
