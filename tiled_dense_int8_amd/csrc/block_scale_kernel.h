@@ -11,7 +11,7 @@
 // 16 rows.
 //
 // Staging.  A and B tiles go to LDS by 16-byte DMA loads with the 16-byte
-// chunks of a row permuted (chunk_swizzle), so that an operand read touches
+// chunks of a row permuted (row16_swizzle), so that an operand read touches
 // every bank once; the tile's a_scale column goes with them by 4-byte DMA.
 // They are buffer loads: one 32-bit offset per lane and a scalar K offset
 // (64-bit addresses would take 16 more registers than a wave has), and what
@@ -30,11 +30,20 @@
 #pragma once
 
 #include "stream_product.h"
-#include "tiled_kernel.h"
 
 namespace tdi8 {
 
 typedef __attribute__((address_space(3))) void lds_void_t;
+
+// Permutation of the 16-byte chunks of row r (128 bytes) for reads of 16 rows
+// by four chunks.  Such a read runs in four passes; measured by bank conflicts,
+// the first takes lanes 0-3, 12-15, 20-23 and 24-27, the second 4-11, 16-19 and
+// 28-31, the others the same 32 lanes on: rows 0-3 and 12-15 at one chunk with
+// rows 4-11 at the next.  Even rows lie in one half of the 256 bytes of all
+// banks, odd ones in the other, so the eight even (odd) ones of a pass must get
+// different chunks: c ^ (r & 2 | 4 (r / 8 & 1)) gives {0, 2, 4, 6} and {1, 3, 5, 7}.
+// (chunk_swizzle, which suits reads of 32 rows, met itself twice in every pass.)
+__device__ __forceinline__ int row16_swizzle(int r) { return (r & 2) | (r >> 1 & 4); }
 
 // One operand of 16 rows x 128, as the instructions take it.
 template <class E>
@@ -108,13 +117,14 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
     // Load i of this wave fills LDS rows 8 (i NW + wave) .. + 7; NW is even, so
     // the chunk permutation is the same for every i.
     const int lrow = wave * 8 + (lane >> 3);
-    const int lchunk = (lane & 7) ^ chunk_swizzle<CPR>((wave & 1) * 8 + (lane >> 3));
+    const int lchunk = (lane & 7) ^ row16_swizzle((wave & 1) * 8 + (lane >> 3));
     const uint32_t off_a = lrow * lda + 16 * lchunk;
     const uint32_t off_b = lrow * ldb + 16 * lchunk;
     // (every wave loads 64 rows' scales, the same ones more than once: a branch
     // here would let the compiler sink the scaled additions behind it)
     const int swave = wave % (BM / 64);
     const uint32_t off_s = (swave * 64 + lane) * static_cast<int>(g.ldas) * 4;
+    constexpr int LOADS = LA + LB + 1;
     auto issue = [&](int kt) {
         int8_t *dst = lds + (kt & 1) * STAGE;
         const int k = kt * BK;
@@ -137,7 +147,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
                                                          : 0));
 
     // LDS offsets of the operand pieces q and 4 + q of row r16.
-    const int sw = chunk_swizzle<CPR>(r16);
+    const int sw = row16_swizzle(r16);
     const int lo_a = (wm * (MT * 16) + r16) * BK + 16 * (q ^ sw);
     const int lo_b = BM * BK + (wn * (NT * 16) + r16) * BK + 16 * (q ^ sw);
     const int ls = SCALES + (wm * (MT * 16) + r16) * 4;
@@ -192,7 +202,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
         for (int i = 0; i < RING; ++i) s[i] = 0.0f;
         // tile 0 has landed when only tile 1's loads are out
         if (nk > 1) {
-            TDI8_WAIT_VMCNT(LA + LB + 1);
+            TDI8_WAIT_VMCNT(LOADS);
         } else {
             TDI8_WAIT_VMCNT(0);
         }
