@@ -18,11 +18,11 @@
 // lies outside the operand, rows past M or N and chunks past K, gets an offset
 // past the buffer's end, which reads as zero.
 //
-// Schedule of a K tile (two stages, one barrier).  Rows 16 i .. 16 i + 15 of
+// Schedule of a K tile (STAGES stages, one barrier).  Rows 16 i .. 16 i + 15 of
 // the wave's part are one step; steps 0 .. MT - 3 read the A operand two steps
 // ahead.  Then every operand of the tile is in registers: the loads of the
-// next tile have landed (issued a whole tile ago), a barrier publishes them
-// and frees this tile's stage, which is refilled at once.  The last two steps
+// next tile have landed (issued STAGES - 1 tiles ago), a barrier publishes
+// them and frees this tile's stage, which is refilled at once.  The last two steps
 // go column by column, and each B operand's registers take the next tile's as
 // soon as both steps are done with it, so the next tile starts with operands
 // in place.  Scaled additions follow three instructions behind the matrix
@@ -71,7 +71,7 @@ struct Operand<F8Wide> {
     }
 };
 
-template <class E, int WM, int WN, int MT, int NT>
+template <class E, int WM, int WN, int MT, int NT, int STAGES>
 __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArgs g) {
     constexpr int NW = WM * WN;
     constexpr int BM = WM * MT * 16, BN = WN * NT * 16;
@@ -82,9 +82,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
     static_assert(BM * CPR % (64 * NW) == 0 && BN * CPR % (64 * NW) == 0 && NW % 2 == 0, "loads split evenly");
     static_assert(BM % 64 == 0 && BM / 64 <= NW, "one scale load per wave");
     static_assert(128 % (NT * 16) == 0 && BN % 128 == 0, "a wave's columns lie in one block of 128");
+    static_assert(STAGES >= 2 && (STAGES & (STAGES - 1)) == 0, "a power of two stages");
+    static_assert((STAGES - 1) * (LA + LB + 1) < 64, "the wait counter holds 63");
     static_assert(MT % 4 == 0, "the operand ring starts over with every tile");
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(1024))) int8_t lds[2 * STAGE];
+    __shared__ __attribute__((aligned(1024))) int8_t lds[STAGES * STAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
     const uint32_t off_s = (swave * 64 + lane) * static_cast<int>(g.ldas) * 4;
     constexpr int LOADS = LA + LB + 1;
     auto issue = [&](int kt) {
-        int8_t *dst = lds + (kt & 1) * STAGE;
+        int8_t *dst = lds + (kt & (STAGES - 1)) * STAGE;
         const int k = kt * BK;
         const uint32_t past = k + 16 * lchunk >= g.K ? kOut : 0u;  // chunks of a last, partial K tile
 #pragma unroll
@@ -168,13 +170,13 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
     f32x4 part[kLag + 1];
     Operand<E> oa[RING];
     auto read_a = [&](int kt, int i) {
-        const int8_t *p = lds + (kt & 1) * STAGE;
+        const int8_t *p = lds + (kt & (STAGES - 1)) * STAGE;
         const i32x4 lo = piece(p + lo_a + i * (16 * BK)), hi = piece(p + (lo_a ^ 64) + i * (16 * BK));
         ra[i % RING] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         rs[i % RING] = *reinterpret_cast<const float *>(p + ls + i * 64);
     };
     auto read_b = [&](int kt, int j) {
-        const int8_t *p = lds + (kt & 1) * STAGE;
+        const int8_t *p = lds + (kt & (STAGES - 1)) * STAGE;
         const i32x4 lo = piece(p + lo_b + j * (16 * BK)), hi = piece(p + (lo_b ^ 64) + j * (16 * BK));
         ob[j].set(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
     };
@@ -194,15 +196,17 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
     static_assert(2 * NT >= kLag + 1 && X % (kLag + 1) == 0, "parts keep their registers from tile to tile");
 
     if (nk > 0) {
-        issue(0);
-        if (nk > 1) issue(1);
+        const int ahead = nk < STAGES ? nk : STAGES;
+#pragma unroll
+        for (int t = 0; t < STAGES; ++t)
+            if (t < ahead) issue(t);
 #pragma unroll
         for (int x = 0; x <= kLag; ++x) part[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < RING; ++i) s[i] = 0.0f;
-        // tile 0 has landed when only tile 1's loads are out
-        if (nk > 1) {
-            TDI8_WAIT_VMCNT(LOADS);
+        // tile 0 has landed when only the later ones' loads are out
+        if (ahead == STAGES) {
+            TDI8_WAIT_VMCNT((STAGES - 1) * LOADS);
         } else {
             TDI8_WAIT_VMCNT(0);
         }
@@ -213,20 +217,27 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
         for (int j = 0; j < NT; ++j) read_b(0, j);
         float sb = scale_b[0];
 
-        // LOAD: refill the freed stage with tile kt + 2; NEXT: tile kt + 1 exists.
-        auto tile = [&](int kt, auto load_tag, auto next_tag) {
+        // LOAD: refill the freed stage with tile kt + STAGES; NEXT: tile kt + 1
+        // exists; INFLIGHT: the loads of tiles kt + 2 .. kt + STAGES - 1 may
+        // stay out while tile kt + 1's are waited for.
+        auto tile = [&](int kt, auto load_tag, auto next_tag, auto inflight_tag) {
             constexpr bool LOAD = decltype(load_tag)::value, NEXT = decltype(next_tag)::value;
+            constexpr bool INFLIGHT = decltype(inflight_tag)::value;
             const float sb_next = NEXT ? scale_b[kt + 1] : 0.0f;
             static_for<X>([&](auto xt) {
                 constexpr int x = decltype(xt)::value;
                 constexpr int i = step_of(x), j = col_of(x);
                 if constexpr (x == TAIL && NEXT) {
                     // every operand of this tile is in registers
-                    TDI8_WAIT_VMCNT(0);
+                    if constexpr (INFLIGHT) {
+                        TDI8_WAIT_VMCNT((STAGES - 2) * LOADS);
+                    } else {
+                        TDI8_WAIT_VMCNT(0);
+                    }
                     TDI8_WAIT_LGKM0();
                     block_barrier();
                     __builtin_amdgcn_sched_barrier(0);
-                    if constexpr (LOAD) issue(kt + 2);
+                    if constexpr (LOAD) issue(kt + STAGES);
                 }
                 if constexpr (x < TAIL && j == 0) read_a(kt, i + 2);
                 if constexpr (j == 0) oa[i % RING].set(ra[i % RING]);
@@ -250,19 +261,20 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
         using T1 = std::true_type;
         using T0 = std::false_type;
         int kt = 0;
-        for (; kt + 2 < nk; ++kt) tile(kt, T1{}, T1{});
-        if (kt + 1 < nk) {
-            tile(kt, T0{}, T1{});
+        for (; kt + STAGES < nk; ++kt) tile(kt, T1{}, T1{}, T1{});
+        if (kt + STAGES == nk && kt + 1 < nk) {
+            tile(kt, T0{}, T1{}, T1{});
             ++kt;
         }
-        tile(kt, T0{}, T0{});
+        for (; kt + 1 < nk; ++kt) tile(kt, T0{}, T1{}, T0{});
+        tile(kt, T0{}, T0{}, T0{});
         static_for<kLag>([&](auto xt) { add(X - kLag + decltype(xt)::value); });
     }
 
     // C through LDS in passes of 64 rows, whole rows of the tile to a wave's
     // stores (rows padded so that an instruction's writes spread over the banks).
     constexpr int RS = BN + 4, RP = 64;
-    static_assert(RP * RS * 4 <= 2 * STAGE, "a pass fits the stages");
+    static_assert(RP * RS * 4 <= STAGES * STAGE, "a pass fits the stages");
     float *cl = reinterpret_cast<float *>(lds);
     for (int p0 = 0; p0 < BM; p0 += RP) {
         __syncthreads();

@@ -1,19 +1,13 @@
 // C ABI entry points of the 8-bit layer operators: argument checks, choice of
 // the kernel, launch.
-#include <cmath>
-
+#include <algorithm>
 #include <climits>
-#include <cstdlib>
+#include <cmath>
 
 #include "abi_common.h"
 #include "product_table.h"
 #include "quant_rows.h"
 
-#ifndef STREAM_ROWS
-#define STREAM_ROWS 32
-#define T128 96
-#define T256 192
-#endif
 namespace tdi8 {
 namespace {
 
@@ -218,32 +212,60 @@ int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
     if (st != TDI8_OK) return st;
     const bool al = aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 16 == 0 && g.ldb % 16 == 0 && g.K % 16 == 0 &&
                     (g.G == 1 || g.group_b % 16 == 0);
-    const int64_t rows = g.offsets ? (static_cast<int64_t>(g.M) + g.G - 1) / g.G : g.M;  // of a group, on average
-    const void *kernel;
-    int bm, bn, threads;
-    // e4m3 tiles address their operands by 32-bit offsets
-    const bool near = !f8 || (256 * (g.lda > g.ldb ? g.lda : g.ldb) + g.K < INT_MAX && 256 * 4 * g.ldas + 4 * g.K < INT_MAX);
-    if (al && near && rows > STREAM_ROWS) {
-        const int tile = rows > T256 ? 2 : rows > T128 ? 1 : 0;
-        const LdsTile t = tile_set(f8, g.type).tile[tile];
-        kernel = tile_set(f8, g.type).kernel[tile];
-        bm = t.bm;
-        bn = t.bn;
-        threads = t.threads;
-    } else {
-#ifdef MANY
-        static const int tile = atoi(getenv("STILE"));
-#else
-        const int tile = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
-#endif
+    // The choice goes by the sizes alone: how the rows fall to the groups is
+    // known to the device only.
+    const int64_t groups = g.G < g.M ? g.G : g.M;  // that can have rows
+    const int64_t rows = (g.M + groups - 1) / groups;
+    // row tiles of height bm: half a tile of each group is lost on average
+    auto expected = [&](int bm, int bn) {
+        const int64_t m = groups == 1 ? (g.M + bm - 1) / bm : std::max<int64_t>(groups, g.M / bm + groups / 2);
+        return m * ((g.N + bn - 1) / bn);
+    };
+    const bool near = !f8 || (256 * std::max(g.lda, g.ldb) + g.K < INT_MAX && 4 * (256 * g.ldas + g.K) < INT_MAX);
+    const ProductKernels &pk = *product_kernels(f8, g.type);
+    const void *kernel = nullptr;
+    int bm = 0, bn = 0, threads = 0;
+    // Stream kernels: few tiles for the chip (64 x 4096 x 4096 e4m3: 12 us
+    // against 22 with 32 tiles of 64 x 128; with 86 tiles, N = 11008, 30
+    // against 20), or so few rows that B is read once anyway.  Several rows a
+    // group go to the LDS tiles even where they are few: groups differ in size,
+    // and a second row tile reads B again (64 groups of 16 rows on average,
+    // 2048 x 2048: 86 us against 54).
+    if (3 * expected(64, 128) < units || rows <= 1 || (groups == 1 && rows <= 16)) {
+        int tile = rows <= 16 ? 0 : rows <= 32 ? 2 : rows <= 64 ? 3 : 4;
+        // with few blocks more waves a block (1024 x 8192 x 16 e4m3: 11.0 and
+        // 11.2 us; 16 x 4096 x 4096 7.5 and 7.6), with many fewer (64 groups
+        // of a row, 4096 x 2048: 100 and 66 us)
+        if (tile == 0 && expected(16, 16) <= units) tile = 1;
         const StreamTile t = kStreamTile[tile];
-        kernel = product_kernels(f8, g.type)->stream[tile][al ? 1 : 0];
+        kernel = pk.stream[tile][al ? 1 : 0];
         bm = t.bm;
         bn = t.bn;
         threads = 64 * t.waves;
+    } else if (!al || !near) {
+        kernel = pk.staged;
+        bm = kStagedTile.bm;
+        bn = kStagedTile.bn;
+        threads = kStagedTile.threads;
+    } else {
+        // the least of the tiles' measured costs; equal ones to the first
+        const TileSet &set = tile_set(f8, g.type);
+        float best = 0.0f;
+        for (int i = 0; i < kLdsTiles && set.kernel[i]; ++i) {
+            const LdsTile &t = set.tile[i];
+            const int64_t round = static_cast<int64_t>(units) * t.per_cu;
+            const int64_t rounds = (expected(t.bm, t.bn) + round - 1) / round;
+            const float cost = rounds * (t.fixed + t.per_4096 * g.K / 4096.0f);
+            if (!kernel || cost < best) {
+                best = cost;
+                kernel = set.kernel[i];
+                bm = t.bm;
+                bn = t.bn;
+                threads = t.threads;
+            }
+        }
     }
     // every group that has rows ends in at most one partial tile
-    const int64_t groups = g.G < g.M ? g.G : g.M;
     const int64_t tm = (g.M + groups * (bm - 1)) / bm;
     const int64_t tn = (static_cast<int64_t>(g.N) + bn - 1) / bn;
     if (tm > INT_MAX || tm * tn > INT_MAX / threads - 8) return TDI8_ERR_INVALID_VALUE;

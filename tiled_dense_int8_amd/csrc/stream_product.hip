@@ -1,7 +1,7 @@
 // Instantiates the stream kernels of one operand type (TDI8_PRODUCT_TYPE, set on
 // the compiler command line: S8, F8 or F8Wide) and registers the type's kernels.
 #include "product_table.h"
-#include "stream_product.h"
+#include "staged_product.h"
 
 #ifndef TDI8_PRODUCT_TYPE
 #error "TDI8_PRODUCT_TYPE must name an operand type and TDI8_PRODUCT_REGISTER its registration function"
@@ -19,6 +19,9 @@ static void register_stream(ProductKernels *k) {
     if constexpr (T + 1 < kStreamTiles) register_stream<T + 1>(k);
 }
 
-void TDI8_PRODUCT_REGISTER(ProductKernels *k) { register_stream<0>(k); }
+void TDI8_PRODUCT_REGISTER(ProductKernels *k) {
+    register_stream<0>(k);
+    k->staged = reinterpret_cast<const void *>(&staged_product_kernel<TDI8_PRODUCT_TYPE, 2, 2, 2, 4>);
+}
 
 }  // namespace tdi8
