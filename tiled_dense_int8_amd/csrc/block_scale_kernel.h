@@ -103,6 +103,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
     const int m0 = (first + within % grows) * BM;
     const int n0 = (within / grows) * BN;
     const int nk = (g.K + BK - 1) / BK;
+    // With one row tile each block reads its part of B alone, and starts at a
+    // K tile of its own (rc_pipelined_kernel.h, the grouped source).
+    const int turn = g.tiles_m == 1 && nk > 0 ? 5 * static_cast<int>(blockIdx.x >> 3) % nk : 0;
+    auto turned = [&](int kt) { return kt + turn < nk ? kt + turn : kt + turn - nk; };
 
     // Buffers over the tile's rows.  A row past M or N starts past the end of
     // its buffer (lda >= K), and so does kOut.
@@ -129,7 +133,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
     constexpr int LOADS = LA + LB + 1;
     auto issue = [&](int kt) {
         int8_t *dst = lds + (kt & (STAGES - 1)) * STAGE;
-        const int k = kt * BK;
+        const int kk = turned(kt);
+        const int k = kk * BK;
         const uint32_t past = k + 16 * lchunk >= g.K ? kOut : 0u;  // chunks of a last, partial K tile
 #pragma unroll
         for (int i = 0; i < LA; ++i)
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
             __builtin_amdgcn_raw_ptr_buffer_load_lds(buf_b, (lds_void_t *)(dst + BM * BK + (i * NW + wave) * 1024), 16,
                                                      static_cast<int>((off_b + i * (NW * 8) * ldb) | past), k, 0, 0);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(buf_s, (lds_void_t *)(dst + SCALES + swave * 256), 4,
-                                                 static_cast<int>(off_s), kt * 4, 0, 0);
+                                                 static_cast<int>(off_s), kk * 4, 0, 0);
     };
     // This wave's scales of B: one block of 128 columns, read as scalars.
     typedef const __attribute__((address_space(4))) float *scalar_t;
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
         read_a(0, 1);
 #pragma unroll
         for (int j = 0; j < NT; ++j) read_b(0, j);
-        float sb = scale_b[0];
+        float sb = scale_b[turn];
 
         // LOAD: refill the freed stage with tile kt + STAGES; NEXT: tile kt + 1
         // exists; INFLIGHT: the loads of tiles kt + 2 .. kt + STAGES - 1 may
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
         auto tile = [&](int kt, auto load_tag, auto next_tag, auto inflight_tag) {
             constexpr bool LOAD = decltype(load_tag)::value, NEXT = decltype(next_tag)::value;
             constexpr bool INFLIGHT = decltype(inflight_tag)::value;
-            const float sb_next = NEXT ? scale_b[kt + 1] : 0.0f;
+            const float sb_next = NEXT ? scale_b[turned(kt + 1)] : 0.0f;
             static_for<X>([&](auto xt) {
                 constexpr int x = decltype(xt)::value;
                 constexpr int i = step_of(x), j = col_of(x);

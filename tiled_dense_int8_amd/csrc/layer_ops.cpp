@@ -231,12 +231,18 @@ int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
     // group go to the LDS tiles even where they are few: groups differ in size,
     // and a second row tile reads B again (64 groups of 16 rows on average,
     // 2048 x 2048: 86 us against 54).
-    if (3 * expected(64, 128) < units || rows <= 1 || (groups == 1 && rows <= 16)) {
-        int tile = rows <= 16 ? 0 : rows <= 32 ? 2 : rows <= 64 ? 3 : 4;
-        // with few blocks more waves a block (1024 x 8192 x 16 e4m3: 11.0 and
-        // 11.2 us; 16 x 4096 x 4096 7.5 and 7.6), with many fewer (64 groups
-        // of a row, 4096 x 2048: 100 and 66 us)
-        if (tile == 0 && expected(16, 16) <= units) tile = 1;
+    const int64_t lds = expected(64, 128);
+    if (3 * lds < units || rows <= 1 || (groups == 1 && rows <= 16 && lds < units)) {
+        // One block of 16 columns for each compute unit or less: more waves a
+        // block (16 x 1024 x 8192 int8 14 -> 11.5 us).  More blocks: fewer, of
+        // 32 columns where the rows differ, which halves what is read of A
+        // (16 x 65536 x 4096 e4m3 76 -> 57 us; 64 groups of a row, 4096 x 2048
+        // int8 71 -> 62; but 1 x 32768 x 4096 e4m3 27 -> 32).
+        int tile = rows <= 16 ? 2 : rows <= 32 ? 3 : rows <= 64 ? 4 : 5;
+        if (tile == 2 && expected(16, 16) <= units)
+            tile = 1;
+        else if (tile == 2 && groups == 1 && rows <= 4)
+            tile = 0;
         const StreamTile t = kStreamTile[tile];
         kernel = pk.stream[tile][al ? 1 : 0];
         bm = t.bm;

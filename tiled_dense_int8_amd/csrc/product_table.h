@@ -7,12 +7,12 @@ namespace tdi8 {
 
 // Stream kernels (stream_product.h): block tile, waves sharing K, chunks that
 // a wave loads at once.
-enum { kStreamTiles = 5 };
+enum { kStreamTiles = 6 };
 struct StreamTile {
     int bm, bn, waves, batch;
 };
 constexpr StreamTile kStreamTile[kStreamTiles] = {
-    {16, 16, 4, 4}, {16, 16, 8, 4}, {32, 16, 8, 2}, {32, 32, 4, 2}, {64, 32, 8, 1}};
+    {16, 16, 4, 4}, {16, 16, 8, 4}, {16, 32, 4, 2}, {32, 16, 8, 2}, {32, 32, 4, 2}, {64, 32, 8, 1}};
 
 // Tiles of the kernels that stage both operands in LDS, and what they were
 // measured to take: a round of `per_cu` blocks on every compute unit costs

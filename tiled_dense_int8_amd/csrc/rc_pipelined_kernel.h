@@ -90,7 +90,7 @@ constexpr int step_group(int ks, int f) {
 template <int MF, int WM, int WN, int MT, int NT, int BK, int STAGES, bool BROW, bool SPLIT, bool EDGE, int SRC,
           bool PERSIST = false>
 __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvParams &cv, int nblocks = 1,
-                                               const ProductArgs *pr = nullptr, RowTile at = {0, 0, 0}, int at_n = 0) {
+                                               const ProductArgs *pr = nullptr, RowTile at = {}, int at_n = 0) {
     static_assert(SRC == 0 || (!BROW && !SPLIT), "the other sources are column-major B, unsplit");
     static_assert(SRC != 2 || (EDGE && MF == 32), "the grouped source: groups end inside tiles");
     static_assert(!PERSIST || (SRC == 0 && !SPLIT && !EDGE && MF == 32), "persistent form: whole tiles, GEMM");
@@ -164,6 +164,13 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
     // multiple of 16, completed the same way.
     const int nk = SRC != 1 ? (kslice + BK - 1) / BK : (cv.rsc + BK - 1) / BK;
 
+    // Grouped: where one block reads a group's whole B tile column by itself,
+    // the blocks start at different K tiles.  In step they would all read the
+    // same K of rows a power of two apart, which lie in few memory channels (32
+    // groups of 32 rows, 2048 x 4096: 91 us in step, 55 spread; K = 4224: 53
+    // either way).  Blocks that share operands stay in step, for the cache
+    // (4096^3: 72 us in step, 77 to 87 spread).
+    [[maybe_unused]] const int first_kt = SRC == 2 && nk > 0 && g.M - at.begin <= BM ? at.turn % nk : 0;
     // Per-lane source pointers of this wave's load instructions (K offset 0).
     // GEMM: chunks outside the operands read the zero chunk: A rows past M,
     // column-major B rows past N, row-major B columns past N, and chunks at
@@ -251,6 +258,9 @@ __device__ __forceinline__ void pipelined_body(const GemmArgs &g, const ConvPara
         if constexpr (PERSIST) {
             const bool is_a = i < A_CHUNKS / 64 / NW;
             return src[i] + (is_a ? la : lb) + koff(i, lt);
+        } else if constexpr (SRC == 2) {
+            const int t = kt + first_kt < nk ? kt + first_kt : kt + first_kt - nk;
+            return t * BK < klim[i] ? src[i] + koff(i, t) : zero_chunk;
         } else if constexpr (SRC != 1 && EDGE) {
             return kt * BK < klim[i] ? src[i] + koff(i, kt) : zero_chunk;
         } else if constexpr (SRC == 0) {
@@ -794,7 +804,7 @@ __global__ void __launch_bounds__(WM * WN * 64) conv_implicit_kernel(GemmArgs g,
 template <int MF, int WM, int WN, int MT, int NT, int BK, int STAGES>
 __global__ void __launch_bounds__(WM * WN * 64) grouped_pipelined_kernel(ProductArgs p) {
     constexpr int BM = WM * MF * MT, BN = WN * MF * NT;
-    RowTile rt{0, 0, 0};
+    RowTile rt{};
     int tiles = 0;
     find_rows(p, BM, -1, rt, &tiles);
     const int64_t total = static_cast<int64_t>(tiles) * p.tiles_n;
@@ -805,6 +815,7 @@ __global__ void __launch_bounds__(WM * WN * 64) grouped_pipelined_kernel(Product
     const int rows = min(tiles - first, 4);
     const int within = static_cast<int>(l % gsize);
     if (!find_rows(p, BM, first + within % rows, rt, nullptr)) return;
+    rt.turn = 5 * static_cast<int>(blockIdx.x >> 3);  // neighbours of an XCD apart
     GemmArgs g{};
     g.A = p.A;
     g.B = p.B + rt.group * p.group_b;

@@ -25,9 +25,10 @@ struct ProductArgs {
     int tiles_m, tiles_n;    // tiles of the grid: tiles_m bounds the groups' row tiles
 };
 
-// The rows [m0, m0 + BM) within one group, as far as `end`.
+// The rows [m0, m0 + BM) within one group, [begin, end).
 struct RowTile {
-    int group, m0, end;
+    int group, m0, begin, end;
+    int turn;  // the K tile to start with (mod their number), where that is free
 };
 
 // Row tile `tile` of the groups' tiles in order (ceil(rows / BM) for each
@@ -38,7 +39,7 @@ __device__ __forceinline__ bool find_rows(const ProductArgs &g, int bm, int tile
     if (!g.offsets) {
         const int tiles = (g.M + bm - 1) / bm;
         if (count) *count = tiles;
-        out = {0, tile * bm, g.M};
+        out = {0, tile * bm, 0, g.M, 0};
         return tile < tiles;
     }
     const int lane = threadIdx.x & 63;
@@ -63,7 +64,8 @@ __device__ __forceinline__ bool find_rows(const ProductArgs &g, int bm, int tile
             const int l = __builtin_ctzll(__ballot(before + sum > tile));
             const int first = before + __builtin_amdgcn_readlane(sum - tiles, l);
             out.group = base + l;
-            out.m0 = __builtin_amdgcn_readlane(lo, l) + (tile - first) * bm;
+            out.begin = __builtin_amdgcn_readlane(lo, l);
+            out.m0 = out.begin + (tile - first) * bm;
             out.end = __builtin_amdgcn_readlane(hi, l);
             found = true;
             if (!count) return true;

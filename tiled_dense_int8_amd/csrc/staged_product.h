@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) staged_product_kernel(Product
     const int wm = wave / WN, wn = wave % WN;
     const int r16 = lane & 15, q = lane >> 4;
 
-    RowTile rt{0, 0, 0};
+    RowTile rt{};
     int tiles = 0;
     find_rows(g, BM, -1, rt, &tiles);
     const int64_t total = static_cast<int64_t>(tiles) * g.tiles_n;

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
     if (at >= total) return;
     // row tiles of one column tile follow each other: they share B
     const int tn = static_cast<int>(at / g.tiles_m);
-    RowTile rt;
+    RowTile rt{};
     if (!find_rows(g, BM, static_cast<int>(at - static_cast<int64_t>(tn) * g.tiles_m), rt, nullptr)) return;
     const int n0 = tn * BN;
 
@@ -130,12 +130,6 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
             return load16_masked(p + k, clamp16(g.K - k));
     };
     const int whole = g.K / kChunk;
-#ifdef ROT
-    const int first = whole > 0 ? tn ROT % whole : 0;
-    auto turn = [&](int c) { c += first; return c >= whole && c - first < whole ? c - whole : c - (c - first >= whole ? first : 0); };
-#else
-    auto turn = [&](int c) { return c; };
-#endif
     // U chunks a time, all of their loads before the first product: a wave has
     // U (MT + NT) KiB on the way at once.
     auto chunks = [&](int kc, auto count, auto whole) {
@@ -144,8 +138,7 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
         float s[C][MT];
 #pragma unroll
         for (int u = 0; u < C; ++u) {
-            const int ck = turn(kc + u * W);
-            const int k = ck * kChunk + 16 * q;
+            const int k = (kc + u * W) * kChunk + 16 * q;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 b[u][j][0] = load(pb[j], k, whole);
@@ -155,7 +148,7 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
             for (int i = 0; i < MT; ++i) {
                 a[u][i][0] = load(pa[i], k, whole);
                 a[u][i][1] = load(pa[i], k + 64, whole);
-                s[u][i] = E::kBlockScales ? psa[i][ck] * psb[ck] : 0.0f;
+                s[u][i] = E::kBlockScales ? psa[i][kc + u * W] * psb[kc + u * W] : 0.0f;
             }
         }
         __builtin_amdgcn_sched_barrier(0);
