@@ -351,11 +351,11 @@ int conv2d_validate(int N, int H, int W, int C, int K, int R, int S,
  *   f8  8-bit floating point (e4m3: 4 exponent and 3 mantissa bits, largest
  *       value 448, no infinity) with one scale per row and block of 128
  *       columns (the last block may be shorter): scale = max|y| / 448.
- * s8 rows are exact: q is the integer nearest to the real quotient, whatever
- * the order of the sums (values next to a border between two integers are
- * decided in 64 bits) and scale is computed in 64 bits and rounded once.  f8
- * rows take their values in 32 bits: the quotient that is rounded to e4m3 is
- * off by less than 2^-19, the scale by less than 2^-20 (relative).
+ * q is exact: the integer (e4m3 value) nearest to the real quotient, ties to
+ * even, whatever the order of the sums: values next to a border between two
+ * are decided in 64 bits.  s8 scales are computed in 64 bits and rounded once;
+ * f8 scales of the activation, and of the norm of 32-bit values, come from the
+ * 32-bit form of the largest value and are off by less than 2^-20.
  * A row (f8: a block) of zeros gets q = 0 and scale = 0; one that holds an
  * infinity or NaN gets q = 0 and scale = NaN.
  *

@@ -54,30 +54,28 @@ def quantise(v, inv, fmt):
     return quotients, torch.stack(scales, 1)
 
 
+def e4m3_nearest(t):
+    """64-bit values up to 448 rounded to e4m3 (3 mantissa bits, exponents from -6 on), ties to even."""
+    _, exponent = torch.frexp(t)  # t = f * 2^exponent, 1/2 <= |f| < 1
+    step = torch.exp2(((exponent - 1).clamp(min=-6) - 3).double())
+    return torch.round(t / step) * step
+
+
 def check_quantised(q, scale, v, inv, fmt, what, steps=10):
     """q and scale against the quotients in 64 bits.
 
-    `steps`: by how many times 2^-24 a 32-bit value v may be off (relative):
-    10 for the activation, 1 for the norm's product of 32-bit values, 0 for
-    that of 16-bit values, which is exact in 32 bits.
-    s8: equal to the nearest integer, ties to even; the scale is computed in
-    64 bits and rounded once to fp32, half a step = 2^-24 relative (values in
-    fp32's normal range), plus what two 64-bit computations differ by
-    (< 2^-40).
-    f8: the largest value of a block is a 32-bit one, so the scale is off by
-    `steps` more; the quotient v * (448 / largest) by that twice and its two
-    operations: at most 22 * 2^-24 < 2^-19.  q is the e4m3 value of a
-    quotient that near to the exact one."""
+    q: equal to the integer, or e4m3 value, nearest to the quotient, ties to
+    even.  scale: computed in 64 bits and rounded once to fp32, half a step =
+    2^-24 relative (values in fp32's normal range), plus what two 64-bit
+    computations differ by (< 2^-40).  f8: a block's largest value may be a
+    32-bit one, off by `steps` times 2^-24: 10 for the activation, 1 for the
+    norm's product of 32-bit values, 0 for that of 16-bit values, which is
+    exact in 32 bits."""
     t, want = quantise(v, inv, fmt)
-    if fmt == "s8":
-        bad = (q.cpu().double() != t.round()).nonzero()
-        assert not len(bad), f"{what}: {len(bad)} values differ, first at {bad[0].tolist()}"
-        scale = scale.reshape(-1, 1)
-    else:
-        got = q.cpu().float()
-        near = [(t * (1 + d)).float().clamp(-448, 448).to(torch.float8_e4m3fn).float() for d in (-2.0 ** -19, 0, 2.0 ** -19)]
-        ok = (got == near[0]) | (got == near[1]) | (got == near[2])
-        assert ok.all(), f"{what}: {(~ok).sum()} values differ, first at {(~ok).nonzero()[0].tolist()}"
+    nearest = t.round() if fmt == "s8" else e4m3_nearest(t)
+    bad = (q.cpu().double() if fmt == "s8" else q.cpu().float().double()) != nearest
+    assert not bad.any(), f"{what}: {bad.sum()} values differ, first at {bad.nonzero()[0].tolist()}"
+    scale = scale.reshape(-1, 1) if fmt == "s8" else scale
     off = (scale.cpu().double() - want).abs()
     allowed = 2.0 ** -24 * (1 + (steps if fmt == "f8" else 0)) + 2.0 ** -40
     assert (off <= want * allowed).all(), f"{what}: scales off by {(off / want).max()}"

@@ -379,58 +379,92 @@ def swiglu_quant_f8(type, T, N, gate, ldg, up, ldu, q, ldq, scale, lds, stream=0
     return _lib.swiglu_quant_f8(type, T, N, gate, ldg, up, ldu, q, ldq, scale, lds, stream)
 
 
-def _call(dev, fn, *args, stream) -> None:
-    """fn(*args, stream handle) with the tensors' device current; raises TDI8Error."""
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream_handle(stream))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream_handle(stream))
+# The wrappers below are called for single tokens, where their own time is what
+# counts: they look at each tensor once and call the library directly.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(index: int, fn, args, stream) -> None:
+    """fn(*args, stream handle) with device `index` current; raises TDI8Error."""
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return _call(index, fn, args, stream)
+    st = fn(*args, _current_stream(index) if stream is None else _stream_handle(stream))
     if st != OK:
         raise TDI8Error(st)
 
 
-def _ld(t) -> int:
-    """Leading dimension of a 2-D tensor with unit column stride (a single row may have any)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _gpu(*tensors) -> int:
+    """Index of the one GPU holding every tensor (None skipped)."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != index or index < 0):
+            _device_of(*(t for t in tensors if t is not None))  # says what is wrong
+            raise ValueError("tensors must be on one GPU")
+    return index
 
 
-def _matrix(name, t, dtype, shape=None) -> None:
+def _fit(*values) -> None:
+    if max(values) > INT_MAX:
+        raise ValueError(f"a size or stride of {max(values)} does not fit the library's int arguments (< 2**31)")
+
+
+def _matrix(name, t, dtype, shape=None) -> int:
+    """Checks a 2-D tensor with unit column stride; its leading dimension."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with unit column stride")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}'s rows overlap")
+    rows, cols = size = t.shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(size)}")
+    if rows > 1:
+        if ld < cols:
+            raise ValueError(f"{name}'s rows overlap")
+        return ld
+    return cols if cols > 1 else 1
 
 
-def _empty(shape, dtype, dev, stream):
+def _empty(like, shape, dtype, stream):
     """A new tensor of the stream that the call runs on (so that its memory
     is not handed out again while the call still runs)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _eight_bit_out(fmt, T, H, dev, out, scale, stream):
-    """The 8-bit output and its scales: the caller's, checked, or new ones."""
-    if fmt not in ("s8", "f8"):
-        raise ValueError(f"fmt must be 's8' or 'f8', not {fmt!r}")
-    dtype, shape = (torch.int8, (T,)) if fmt == "s8" else (torch.float8_e4m3fn, (T, -(-H // BLOCK)))
-    if out is None:
-        out = _empty((T, H), dtype, dev, stream)
+def _eight_bit_out(fmt, T, H, like, out, scale, stream):
+    """The 8-bit output and its scales, the caller's, checked, or new ones, and their leading dimensions."""
+    if fmt == "s8":
+        dtype, shape = torch.int8, (T,)
+    elif fmt == "f8":
+        dtype, shape = torch.float8_e4m3fn, (T, (H + BLOCK - 1) // BLOCK)
     else:
-        _matrix("out", out, dtype, (T, H))
+        raise ValueError(f"fmt must be 's8' or 'f8', not {fmt!r}")
+    if out is None:
+        out, ldq = _empty(like, (T, H), dtype, stream), max(H, 1)
+    else:
+        ldq = _matrix("out", out, dtype, (T, H))
+    lds = max(shape[-1], 1)
     if scale is None:
-        scale = _empty(shape, torch.float32, dev, stream)
-    elif scale.dtype != torch.float32 or tuple(scale.shape) != shape or (shape[-1] > 1 and scale.stride(-1) != 1):
-        raise ValueError(f"scale must be float32 {shape} with unit stride along its last axis")
-    return out, scale
+        scale = _empty(like, shape, torch.float32, stream)
+    elif fmt == "f8":
+        lds = _matrix("scale", scale, torch.float32, shape)
+    else:
+        _vector("scale", scale, torch.float32, T)
+    return out, ldq, scale, lds
+
+
+def _vector(name, t, dtype, count) -> None:
+    if t.dtype != dtype or t.shape != (count,) or (count > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a dense {dtype} vector of {count} values")
 
 
 def rms_norm(x, weight, eps: float = 1e-6, residual=None, fmt: str = "s8", sum_out=None, out=None, scale=None,
@@ -444,51 +478,52 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, fmt: str = "s8", sum_o
        (T, ceil(H / 128)), one for each block of 128 columns.
     sum_out: where the sum goes (x or residual itself: in place).
     """
-    if x.dtype not in _TYPES:
+    dtype = x.dtype
+    code = _TYPES.get(dtype)
+    if code is None:
         raise TypeError("x must be float32, bfloat16 or float16")
-    _matrix("x", x, x.dtype)
-    T, H = x.shape
-    if weight.dtype != x.dtype or tuple(weight.shape) != (H,) or (H > 1 and weight.stride(0) != 1):
-        raise ValueError(f"weight must be a dense {x.dtype} vector of {H} values")
+    ldx = _matrix("x", x, dtype)
+    T, H = shape = x.shape
+    _vector("weight", weight, dtype, H)
+    ldr = ldsum = 0
     if residual is not None:
-        _matrix("residual", residual, x.dtype, (T, H))
+        ldr = _matrix("residual", residual, dtype, shape)
+        if sum_out is not None:
+            ldsum = _matrix("sum_out", sum_out, dtype, shape)
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    given = [t for t in (x, weight, residual, sum_out, out, scale) if t is not None]
-    dev = _device_of(*given)
-    if residual is not None:
-        if sum_out is None:
-            sum_out = _empty((T, H), x.dtype, dev, stream)
-        else:
-            _matrix("sum_out", sum_out, x.dtype, (T, H))
-    out, scale = _eight_bit_out(fmt, T, H, dev, out, scale, stream)
-    args = [_TYPES[x.dtype], T, H, x.data_ptr(), _ld(x), residual.data_ptr() if residual is not None else None,
-            _ld(residual) if residual is not None else 0, weight.data_ptr(), eps,
-            sum_out.data_ptr() if residual is not None else None, _ld(sum_out) if residual is not None else 0,
-            out.data_ptr(), _ld(out), scale.data_ptr()]
+    index = _gpu(x, weight, residual, sum_out, out, scale)
+    if residual is not None and sum_out is None:
+        sum_out, ldsum = _empty(x, shape, dtype, stream), max(H, 1)
+    out, ldq, scale, lds = _eight_bit_out(fmt, T, H, x, out, scale, stream)
+    _fit(T, H, ldx, ldr, ldsum, ldq, lds)
+    args = (code, T, H, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(),
+            eps, None if residual is None else sum_out.data_ptr(), ldsum, out.data_ptr(), ldq, scale.data_ptr())
     if fmt == "s8":
-        _call(dev, rmsnorm_quant_s8, *args, stream=stream)
+        _call(index, _lib.rmsnorm_quant_s8, args, stream)
     else:
-        _call(dev, rmsnorm_quant_f8, *args, _ld(scale), stream=stream)
+        _call(index, _lib.rmsnorm_quant_f8, args + (lds,), stream)
     return (out, scale) if residual is None else (out, scale, sum_out)
 
 
 def swiglu(gate, up, fmt: str = "s8", out=None, scale=None, stream=None):
     """(q, scale) of gate / (1 + exp(-gate)) * up for gate and up (T, N), in
     the formats of rms_norm; the two may be halves of one tensor's rows."""
-    if gate.dtype not in _TYPES:
+    dtype = gate.dtype
+    code = _TYPES.get(dtype)
+    if code is None:
         raise TypeError("gate must be float32, bfloat16 or float16")
-    _matrix("gate", gate, gate.dtype)
-    T, N = gate.shape
-    _matrix("up", up, gate.dtype, (T, N))
-    dev = _device_of(*(t for t in (gate, up, out, scale) if t is not None))
-    out, scale = _eight_bit_out(fmt, T, N, dev, out, scale, stream)
-    args = [_TYPES[gate.dtype], T, N, gate.data_ptr(), _ld(gate), up.data_ptr(), _ld(up), out.data_ptr(), _ld(out),
-            scale.data_ptr()]
+    ldg = _matrix("gate", gate, dtype)
+    T, N = shape = gate.shape
+    ldu = _matrix("up", up, dtype, shape)
+    index = _gpu(gate, up, out, scale)
+    out, ldq, scale, lds = _eight_bit_out(fmt, T, N, gate, out, scale, stream)
+    _fit(T, N, ldg, ldu, ldq, lds)
+    args = (code, T, N, gate.data_ptr(), ldg, up.data_ptr(), ldu, out.data_ptr(), ldq, scale.data_ptr())
     if fmt == "s8":
-        _call(dev, swiglu_quant_s8, *args, stream=stream)
+        _call(index, _lib.swiglu_quant_s8, args, stream)
     else:
-        _call(dev, swiglu_quant_f8, *args, _ld(scale), stream=stream)
+        _call(index, _lib.swiglu_quant_f8, args + (lds,), stream)
     return out, scale
 
 
@@ -508,20 +543,15 @@ def gemm_f8f8_block128(type, M, N, K, A, lda, a_scale, ldas, B, ldb, b_scale, ld
     return _lib.gemm_f8f8_block128(type, M, N, K, A, lda, a_scale, ldas, B, ldb, b_scale, ldbs, C, ldc, stream)
 
 
-def _vector(name, t, dtype, count) -> None:
-    if t.dtype != dtype or tuple(t.shape) != (count,) or (count > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a dense {dtype} vector of {count} values")
-
-
-def _product_out(M, N, dtype, dev, out, stream):
+def _product_out(M, N, dtype, like, out, stream):
+    """The product's output, the caller's, checked, or a new one, and its leading dimension."""
     if out is None:
         if dtype not in _TYPES:
             raise TypeError("dtype must be float32, bfloat16 or float16")
-        return _empty((M, N), dtype, dev, stream)
+        return _empty(like, (M, N), dtype, stream), max(N, 1)
     if out.dtype not in _TYPES:
         raise TypeError("out must be float32, bfloat16 or float16")
-    _matrix("out", out, out.dtype, (M, N))
-    return out
+    return out, _matrix("out", out, out.dtype, (M, N))
 
 
 def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtype=torch.bfloat16, stream=None):
@@ -537,7 +567,7 @@ def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtyp
     out: (M, N) of a floating type, or dtype for a new tensor; rows from
        offsets[G] on are not written.
     """
-    _matrix("A", A, torch.int8)
+    lda = _matrix("A", A, torch.int8)
     T, K = A.shape
     if B.dtype != torch.int8:
         raise TypeError(f"B must be torch.int8, not {B.dtype}")
@@ -546,22 +576,25 @@ def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtyp
     if B.dim() != 3 or B.shape[2] != K or (K > 1 and B.stride(2) != 1):
         raise ValueError("B must be (G, N, K) or (N, K) with A's K and unit stride along it")
     G, N, _ = B.shape
-    if b_scale.dtype != torch.float32 or tuple(b_scale.shape) != (G, N) or not b_scale.is_contiguous():
+    if b_scale.dtype != torch.float32 or b_scale.shape != (G, N) or not b_scale.is_contiguous():
         raise ValueError(f"b_scale must be a dense float32 tensor of shape {(G, N)}")
     _vector("a_scale", a_scale, torch.float32, T)
     if offsets is not None:
         _vector("offsets", offsets, torch.int32, G + 1)
     elif G != 1:
         raise ValueError("offsets are needed for more than one group")
+    M = T
     if rows is not None:
-        _vector("rows", rows, torch.int32, rows.numel())
-    M = T if rows is None else rows.numel()
-    dev = _device_of(*(t for t in (A, a_scale, B, b_scale, offsets, rows, out) if t is not None))
-    out = _product_out(M, N, dtype, dev, out, stream)
-    _call(dev, gemm_s8s8_grouped, _TYPES[out.dtype], G, M, N, K, A.data_ptr(), _ld(A), T, a_scale.data_ptr(),
-          None if rows is None else rows.data_ptr(), None if offsets is None else offsets.data_ptr(), B.data_ptr(),
-          B.stride(1) if N > 1 else max(K, 1), B.stride(0) if G > 1 else 0, b_scale.data_ptr(), out.data_ptr(),
-          _ld(out), stream=stream)
+        M = rows.numel()
+        _vector("rows", rows, torch.int32, M)
+    index = _gpu(A, a_scale, B, b_scale, offsets, rows, out)
+    out, ldc = _product_out(M, N, dtype, A, out, stream)
+    ldb = B.stride(1) if N > 1 else max(K, 1)
+    _fit(G, M, N, K, lda, T, ldb, ldc)
+    _call(index, _lib.gemm_s8s8_grouped,
+          (_TYPES[out.dtype], G, M, N, K, A.data_ptr(), lda, T, a_scale.data_ptr(),
+           None if rows is None else rows.data_ptr(), None if offsets is None else offsets.data_ptr(), B.data_ptr(),
+           ldb, B.stride(0) if G > 1 else 0, b_scale.data_ptr(), out.data_ptr(), ldc), stream)
     return out
 
 
@@ -573,16 +606,18 @@ def gemm_f8(A, a_scale, B, b_scale, out=None, dtype=torch.bfloat16, stream=None)
     B: float8_e4m3fn (N, K), b_scale: float32 (ceil(N / 128), ceil(K / 128)).
     out: (M, N) of a floating type, or dtype for a new tensor.
     """
-    _matrix("A", A, torch.float8_e4m3fn)
-    _matrix("B", B, torch.float8_e4m3fn)
+    lda = _matrix("A", A, torch.float8_e4m3fn)
+    ldb = _matrix("B", B, torch.float8_e4m3fn)
     (M, K), N = A.shape, B.shape[0]
     if B.shape[1] != K:
         raise ValueError("inner dimensions differ")
-    kb = -(-K // BLOCK)
-    _matrix("a_scale", a_scale, torch.float32, (M, kb))
-    _matrix("b_scale", b_scale, torch.float32, (-(-N // BLOCK), kb))
-    dev = _device_of(*(t for t in (A, a_scale, B, b_scale, out) if t is not None))
-    out = _product_out(M, N, dtype, dev, out, stream)
-    _call(dev, gemm_f8f8_block128, _TYPES[out.dtype], M, N, K, A.data_ptr(), _ld(A), a_scale.data_ptr(), _ld(a_scale),
-          B.data_ptr(), _ld(B), b_scale.data_ptr(), _ld(b_scale), out.data_ptr(), _ld(out), stream=stream)
+    kb = (K + BLOCK - 1) // BLOCK
+    ldas = _matrix("a_scale", a_scale, torch.float32, (M, kb))
+    ldbs = _matrix("b_scale", b_scale, torch.float32, ((N + BLOCK - 1) // BLOCK, kb))
+    index = _gpu(A, a_scale, B, b_scale, out)
+    out, ldc = _product_out(M, N, dtype, A, out, stream)
+    _fit(M, N, K, lda, ldas, ldb, ldbs, ldc)
+    _call(index, _lib.gemm_f8f8_block128,
+          (_TYPES[out.dtype], M, N, K, A.data_ptr(), lda, a_scale.data_ptr(), ldas, B.data_ptr(), ldb,
+           b_scale.data_ptr(), ldbs, out.data_ptr(), ldc), stream)
     return out

@@ -9,16 +9,14 @@
 //         q = e4m3(448 v / max|v|)
 //
 // The norm's root cancels out of q, so q needs the row's (block's) largest
-// |v| only and the root goes into the scale.  s8 is exact: q is the integer
-// nearest to the real quotient (ties to even).  The quotient is first taken
-// in fp32, whose error is below kNear (counted at to_s8); where it lies that
-// near a border between two integers it is taken again in fp64.  Without
-// this, values next to a border would round by the last bit of a sum or an
-// exponential, and two orders of the same computation would give different
-// bytes.  f8 rounds the fp32 quotient (v and the largest |v| are off by at
-// most 10 * 2^-24 each, its two operations by 2^-24: below 2^-19, a step is
-// 2^-3).  The sum of squares is held in fp64: finite inputs cannot overflow
-// it, and it then says whether a row holds an infinity or NaN.
+// |v| only and the root goes into the scale.  q is exact: the integer or e4m3
+// value nearest to the real quotient, ties to even.  The quotient is first
+// taken in fp32 with a known error (kNear, kOff); where it lies that near a
+// border between two values it is taken again in fp64.  Without this, values
+// next to a border would round by the last bit of a sum or an exponential, and
+// two orders of the same computation would give different bytes.  The sum of
+// squares is held in fp64: finite inputs cannot overflow it, and it then says
+// whether a row holds an infinity or NaN.
 //
 // A row (f8: block) that holds an infinity or NaN has q = 0 and scale = NaN,
 // so that products with it come out NaN; one of zeros has q = 0 and scale = 0.
@@ -272,7 +270,7 @@ __device__ __forceinline__ float scale_of(double m, double inv, double top, bool
     return !number ? __builtin_nanf("") : m == 0.0 ? 0.0f : static_cast<float>(m * inv / top);
 }
 
-// How near a border the fp32 quotient counts as undecided: above its error.
+// s8: how near a border the fp32 quotient counts as undecided, above its error.
 // t = v k is rounded with its border test in one step (fused), so it is off by
 // 127 times the relative errors of v (at most 10 * 2^-24, 2^-24, 0 for the
 // activation, the norm of fp32, the norm of 16-bit types), of the maximum's
@@ -280,6 +278,28 @@ __device__ __forceinline__ float scale_of(double m, double inv, double top, bool
 // 12, 3 and 1 times 127 * 2^-24.
 template <class T, int OP>
 constexpr float kNear = OP == kOpAct ? 0x1p-13f : T::kBytes == 4 ? 0x1p-15f : 0x1p-16f;
+// Relative error of the fp32 quotient v k of f8, k = 448 / max|v|: v and the
+// maximum by the errors above (twice 10, 1, 0), k and the product by 2^-24
+// each, its two sides kOff apart by another two: 24, 6 and 4 times 2^-24 at
+// most, the last with an exact maximum (k, its side and the product: 3).
+template <class T, int OP>
+constexpr float kOff = OP == kOpAct ? 0x1p-19f : T::kBytes == 4 ? 0x1p-21f : 0x1p-22f;
+
+// Four fp32 values as e4m3 bytes, nearest, ties to even.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+}
+// x as an e4m3 byte.  The fp32 value between is rounded to odd (towards zero,
+// the last bit set where anything was lost), so that the second rounding sees
+// on which side of a border x lies.
+__device__ __forceinline__ uint32_t e4m3_of(double x) {
+    float f = static_cast<float>(x);
+    if (fabs(static_cast<double>(f)) > fabs(x)) f = __uint_as_float(__float_as_uint(f) - 1u);
+    if (static_cast<double>(f) != x) f = __uint_as_float(__float_as_uint(f) | 1u);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(f, 0.0f, 0, false)) & 0xffu;
+}
+
 // fp32 values from 2^22 up to 2^23 in magnitude plus this have their integer
 // part, rounded to nearest even, in the low mantissa bits.
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
@@ -567,52 +587,67 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
         if (t == 0) g.scale[row] = scale_of(m, root(), 127.0, number);
     } else {
         const double inv = root();
-        each([&](int v, const float *values, auto &&operands) {
+        each([&](int v, const float *f, auto &&operands) {
             const int c = col0 + (v * THREADS + t) * 8;
             const int n = g.cols - c;
-            float f[8];
             uint32_t bits = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[i] = values[i];
-                bits = max(bits, abs_bits(f[i]));
-            }
+            for (int i = 0; i < 8; ++i) bits = max(bits, abs_bits(f[i]));
+            const uint32_t own = bits;
             bits = block128_max(bits);  // lanes past the row hold zeros
-            double m;
+            const bool plain = plain_range(bits);
+            double m = __uint_as_float(bits);
             bool number = true;
-            if (plain_range(bits)) {
-                const float mf = __uint_as_float(bits);
-                const float k = 448.0f / mf;
-                m = mf;
+            uint32_t w2[2] = {0, 0}, diff[2] = {~0u, ~0u};
+            if (plain) {
+                // The quotients a little low and a little high: where both
+                // round to the same bytes those are right.
+                const float k = 448.0f / __uint_as_float(bits);
+                const float low = k * (1.0f - kOff<T, OP>), high = k * (1.0f + kOff<T, OP>);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] *= k;
-            } else {
-                // the 16 lanes of a block come here together
+                for (int h = 0; h < 2; ++h) {
+                    w2[h] = e4m3x4(f[4 * h] * low, f[4 * h + 1] * low, f[4 * h + 2] * low, f[4 * h + 3] * low);
+                    diff[h] = w2[h] ^ e4m3x4(f[4 * h] * high, f[4 * h + 1] * high, f[4 * h + 2] * high,
+                                             f[4 * h + 3] * high);
+                }
+            }
+            // Others are decided in fp64, by all 16 lanes of the block together.
+            const uint64_t undecided = __ballot((diff[0] | diff[1]) != 0);
+            if ((undecided >> (t & 48) & 0xffff) != 0) {
                 Vec8<T> a, b;
                 operands(a, b);
-                const uint64_t m64 = block128_max(max_at64(a, b));
-                m = __builtin_bit_cast(double, m64);
-                number = m64 < kInf64;
+                if (!(plain && OP == kOpNorm && SIZE == 2)) {
+                    // the largest |v|, as for s8
+                    const uint32_t from = plain ? abs_bits(__uint_as_float(bits) * (1.0f - 0x1p-19f)) : 0u;
+                    uint64_t m64 = 0;
+                    if (own >= from) {
+                        uint32_t which = plain ? 0u : 0xffu;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-                if (number && m64 != 0) {
-#pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
-                        const float x = static_cast<float>(value_at(a, b, i) * 448.0 / m);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = i == j ? x : f[j];
+                        for (int i = 0; i < 8; ++i) which |= abs_bits(f[i]) >= from ? 1u << i : 0u;
+                        for (; which != 0; which &= which - 1) {
+                            const int i = __builtin_ctz(which);
+                            const uint64_t o = abs_bits(value64<OP>(a.pick(i), b.pick(i)));
+                            m64 = o > m64 ? o : m64;
+                        }
                     }
+                    m64 = block128_max(m64);
+                    m = __builtin_bit_cast(double, m64);
+                    number = m64 < kInf64;
                 }
+                uint64_t q = static_cast<uint64_t>(w2[1]) << 32 | w2[0];
+                const uint64_t d = static_cast<uint64_t>(diff[1]) << 32 | diff[0];
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    if ((d >> (8 * i) & 0xff) == 0) continue;
+                    const uint32_t byte = number && m != 0.0 ? e4m3_of(value64<OP>(a.pick(i), b.pick(i)) * 448.0 / m) : 0u;
+                    q = (q & ~(0xffull << (8 * i))) | static_cast<uint64_t>(byte) << (8 * i);
+                }
+                w2[0] = static_cast<uint32_t>(q);
+                w2[1] = static_cast<uint32_t>(q >> 32);
             }
             if (n <= 0) return;
             if ((t & 15) == 0) g.scale[row * g.lds + (c >> 7)] = scale_of(m, inv, 448.0, number);
-            int w2[2] = {0, 0};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                w2[h] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h], f[4 * h + 1], 0, false);
-                w2[h] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2], f[4 * h + 3], w2[h], true);
-            }
-            store8_bytes(pq + c, static_cast<uint32_t>(w2[0]), static_cast<uint32_t>(w2[1]), n);
+            store8_bytes(pq + c, w2[0], w2[1], n);
         });
     }
 #endif
