@@ -29,8 +29,9 @@ struct RowShape {
 constexpr RowShape kRowShape[kRowShapes] = {{64, -1}, {64, 1},  {256, 1}, {256, 2}, {256, 3},
                                             {256, 4}, {512, 3}, {512, 4}, {1024, 0}};
 // f8 activations, which need no whole row, take a longer one by blocks of this
-// shape (8192 x 11008: 108 us; one block of 1024 threads per row: 163 us).
-constexpr int kActShape = 3;  // {256, 2}
+// shape (8192 x 11008 bf16: 102 us; by {256, 2} 106, by {256, 1} 118, one block
+// of 1024 threads per row 163).
+constexpr int kActShape = 4;  // {256, 3}
 // Rows that one block computes: the one-wave shape puts four in a block.
 constexpr int rows_per_block(int threads) { return threads == 64 ? 4 : 1; }
 
