@@ -379,7 +379,8 @@ typedef enum {
  * Pointers to `type` are aligned to its size, scale to 4 bytes; leading
  * dimensions are in elements, at least H, and H is at most 2^30
  * (TDI8_ERR_INVALID_VALUE otherwise, also for eps < 0 or not finite and an
- * unknown type).  T == 0 or H == 0 enqueues nothing.  One kernel on `stream`;
+ * unknown type).  T == 0 or H == 0 enqueues nothing.  One kernel on `stream`
+ * (more for over two million rows, by their length);
  * ownership and the other errors as for gemm_s8s8s32. */
 int rmsnorm_quant_s8(int type, int T, int H, const void *x, int ldx, const void *residual, int ldr,
                      const void *weight, float eps, void *sum, int ldsum, int8_t *q, int ldq, float *scale,

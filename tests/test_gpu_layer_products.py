@@ -254,8 +254,54 @@ def test_f8_strides(M, kind):
     run_f8(g, M, 200, 256, kind, start=(9, 0, 5), scale_pad=1)
 
 
-@pytest.mark.parametrize("M", [2, 24, 60, 300])
-def test_f8_special_values(M):
+def test_f8_no_k():
+    for kind in TYPES.values():
+        for M, N in ((3, 5), (40, 300), (300, 20000)):
+            e = torch.empty(M, 0, dtype=torch.float8_e4m3fn, device="cuda")
+            out = torch.full((M, N), SENTINEL, dtype=kind, device="cuda")
+            t.gemm_f8(e, torch.empty(M, 0, device="cuda"), torch.empty(N, 0, dtype=e.dtype, device="cuda"),
+                      torch.empty(-(-N // 128), 0, device="cuda"), out=out)
+            assert (out == 0).all()
+
+
+# (few rows; every LDS tile: 64 x 128 up to 256 x 256, in both forms; unaligned ones)
+LARGE = [(70, 11008, 512), (256, 16384, 256), (1024, 4096, 640), (2100, 4096, 256), (4096, 4096, 384),
+         (333, 16400, 272), (600, 8200, 200)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("size", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_f8_large(size, kind):
+    """Sizes at which the choice takes each kernel, with leading dimensions off the sizes."""
+    run_f8(gen(sum(size)), *size, kind, ld=(16, 0, 8) if size[2] % 16 == 0 else (0, 0, 1))
+
+
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+@pytest.mark.parametrize("case", [([3] * 40, 2048, 256), ([70, 0, 200, 31] * 8, 1024, 256), ([300, 900, 50, 0], 4096, 128),
+                                  ([2500, 1, 1500, 60], 2048, 128), ([130] * 12, 1100, 200), ([1] * 150, 500, 512)],
+                         ids=lambda c: f"{len(c[0])}x{max(c[0])}")
+def test_grouped_large(case, kind):
+    counts, N, K = case
+    run_grouped(gen(N + K + len(counts)), counts, N, K, kind, T=100, slack=5)
+
+
+def test_grouped_many_groups_and_bad_offsets():
+    """More groups than a wave has lanes by far, and offsets whose groups all overlap."""
+    g = gen(12)
+    G, N, K = 5000, 16, 32
+    run_grouped(g, [i % 7 == 0 for i in range(G)], N, K, "bf16")
+    A, sa = s8(g, 4000, K).cuda(), scales(g, 4000).cuda()
+    B, sb = s8(g, G, N, K).cuda(), scales(g, G, N).cuda()
+    bad = (torch.arange(G + 1, dtype=torch.int32) % 2 * 4000).cuda()
+    buf = torch.full((4100, N), SENTINEL, device="cuda")
+    t.grouped_gemm(A, sa, B, sb, bad, out=buf[50:4050])
+    torch.cuda.synchronize()
+    assert (buf[:50] == SENTINEL).all() and (buf[4050:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [2, 24, 60, 300, 3000])
+def test_f8_special_values(M, kind):
     """NaN reaches its row or column, zero scales give zeros, the largest and smallest magnitudes hold."""
     g = gen(20 + M)
     N, K = 150, 400
@@ -264,17 +310,17 @@ def test_f8_special_values(M):
     sa[0] = 0
     bad = A.clone().view(torch.int8)
     bad[1, 399] = 0x7f
-    got = t.gemm_f8(bad.view(torch.float8_e4m3fn).cuda(), sa.cuda(), B.cuda(), sb.cuda(), dtype=torch.float32).cpu()
+    got = t.gemm_f8(bad.view(torch.float8_e4m3fn).cuda(), sa.cuda(), B.cuda(), sb.cuda(), dtype=TYPES[kind]).cpu()
     assert got[1].isnan().all() and (got[0] == 0).all() and not got[torch.arange(M) != 1].isnan().any()
     badb = B.clone().view(torch.int8)
     badb[149, 0] = -1
-    got = t.gemm_f8(A.cuda(), sa.cuda(), badb.view(torch.float8_e4m3fn).cuda(), sb.cuda(), dtype=torch.float32).cpu()
+    got = t.gemm_f8(A.cuda(), sa.cuda(), badb.view(torch.float8_e4m3fn).cuda(), sb.cuda(), dtype=TYPES[kind]).cpu()
     assert got[:, 149].isnan().all() and not got[:, :149].isnan().any()
     for value in (448.0, 2.0 ** -9):
         a = torch.full((M, K), value).to(torch.float8_e4m3fn)
         got = t.gemm_f8(a.cuda(), torch.ones(M, 4).cuda(), a[:1].expand(N, K).contiguous().cuda(),
-                        torch.ones(2, 4).cuda(), dtype=torch.float32).cpu()
-        assert (got == value * value * K).all()
+                        torch.ones(2, 4).cuda(), dtype=TYPES[kind]).cpu()
+        assert (got == torch.tensor(value * value * K).to(TYPES[kind])).all()
 
 
 def test_f8_far_operands():

@@ -239,3 +239,16 @@ def test_graph_and_streams():
         e2 = t.swiglu(e[2], x)
         for a, b in ((q, e[0]), (s, e[1]), (y, e[2]), (q2, e2[0]), (s2, e2[1])):
             assert torch.equal(a, b)
+
+
+def test_more_rows_than_a_grid_holds():
+    """Rows past one launch's 2^31 threads; every row by its own length-1 definition: q = 127 sign(x)."""
+    T = 2 ** 25 + 70_000
+    x = torch.randn(T, 1, device="cuda")
+    q, scale = t.rms_norm(x, torch.ones(1, device="cuda"), 0.0)
+    assert torch.equal(q, (127 * torch.sign(x)).to(torch.int8))
+    want = (x[:, 0] != 0).float()  # zeros, which so many normal values contain, have scale 0
+    assert ((scale * 127 - want).abs() <= 2 ** -22).all()
+    q, scale = t.swiglu(x, x, fmt="f8")
+    assert torch.equal(q.float(), (448 * torch.sign(x * x)))
+    assert scale.shape == (T, 1) and scale[-1] > 0 and scale.isfinite().all()

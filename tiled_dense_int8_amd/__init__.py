@@ -381,8 +381,9 @@ def swiglu_quant_f8(type, T, N, gate, ldg, up, ldu, q, ldq, scale, lds, stream=0
 
 # The wrappers below are called for single tokens, where their own time is what
 # counts: they look at each tensor once and call the library directly.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(index: int, fn, args, stream) -> None:

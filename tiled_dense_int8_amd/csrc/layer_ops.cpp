@@ -91,12 +91,30 @@ int rows_entry(int op, int fmt, int type, RowArgs g, hipStream_t stream) {
         shape = kRowShapes - 1;
         parts = 1;
     }
+    const int threads = kRowShape[shape].threads * rows_per_block(kRowShape[shape].threads);
     const int per = rows_per_block(kRowShape[shape].threads);
-    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(g.rows) + per - 1) / per);
-    void *args[] = {&g};
-    const hipError_t e = hipLaunchKernel(row_kernels(type)->kernel[shape][op][fmt], dim3(blocks, parts),
-                                         dim3(kRowShape[shape].threads * per), args, 0, stream);
-    return e == hipSuccess ? TDI8_OK : hip_fail(e);
+    // a grid holds fewer than 2^32 threads: more rows take more launches
+    const int64_t most = static_cast<int64_t>(INT_MAX / threads) * per;
+    const int64_t size = type_bytes(type), rows = g.rows;
+    const int64_t scales = fmt == kFmtS8 ? 1 : g.lds;
+    const RowArgs all = g;
+    for (int64_t first = 0; first < rows; first += most) {
+        auto at = [&](const void *p, int64_t ld) {
+            return p ? static_cast<const char *>(p) + first * ld * size : nullptr;
+        };
+        g.a = at(all.a, all.lda);
+        g.b = at(all.b, all.ldb);
+        g.sum = const_cast<char *>(at(all.sum, all.ldsum));
+        g.q = static_cast<char *>(all.q) + first * all.ldq;
+        g.scale = all.scale + first * scales;
+        g.rows = static_cast<int>(std::min(rows - first, most));
+        const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(g.rows) + per - 1) / per);
+        void *args[] = {&g};
+        const hipError_t e = hipLaunchKernel(row_kernels(type)->kernel[shape][op][fmt], dim3(blocks, parts),
+                                             dim3(threads), args, 0, stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+    return TDI8_OK;
 }
 
 int norm_entry(int fmt, int type, int T, int H, const void *x, int ldx, const void *residual, int ldr,

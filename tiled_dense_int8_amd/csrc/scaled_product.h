@@ -34,17 +34,21 @@ struct RowTile {
 // Row tile `tile` of the groups' tiles in order (ceil(rows / BM) for each
 // group), and how many there are.  Every wave searches by itself: 64 offsets a
 // step, a prefix sum over the lanes.  Offsets are clamped to [0, M] and to
-// rising order, so that no value of theirs leads outside C.
+// rising order within each group, so that no value of theirs leads outside C;
+// groups that overlap all the same could count past any bound, so the sums
+// stop at kMostTiles (at most M + G <= 2^31 tiles of at least a row are asked
+// for, of which disjoint groups have at most 2^30).
+constexpr uint32_t kMostTiles = 1u << 30;
 __device__ __forceinline__ bool find_rows(const ProductArgs &g, int bm, int tile, RowTile &out, int *count) {
     if (!g.offsets) {
         const int tiles = (g.M + bm - 1) / bm;
         if (count) *count = tiles;
         out = {0, tile * bm, 0, g.M, 0};
-        return tile < tiles;
+        return tile >= 0 && tile < tiles;
     }
     const int lane = threadIdx.x & 63;
-    int before = 0;
-    bool found = false;
+    uint32_t before = 0;
+    bool found = tile < 0;
     for (int base = 0; base < g.G; base += 64) {
         const int e = base + lane;
         int lo = 0, hi = 0;
@@ -52,28 +56,28 @@ __device__ __forceinline__ bool find_rows(const ProductArgs &g, int bm, int tile
             lo = min(max(g.offsets[e], 0), g.M);
             hi = min(max(g.offsets[e + 1], lo), g.M);
         }
-        const int tiles = (hi - lo + bm - 1) / bm;
-        int sum = tiles;
+        const uint32_t tiles = static_cast<uint32_t>(hi - lo + bm - 1) / bm;
+        uint32_t sum = tiles;
 #pragma unroll
         for (int s = 1; s < 64; s <<= 1) {
-            const int o = __shfl_up(sum, s);
-            if (lane >= s) sum += o;
+            const uint32_t o = static_cast<uint32_t>(__shfl_up(static_cast<int>(sum), s));
+            if (lane >= s) sum = min(sum + o, kMostTiles);
         }
-        const int total = __builtin_amdgcn_readlane(sum, 63);
-        if (!found && tile - before < total) {
-            const int l = __builtin_ctzll(__ballot(before + sum > tile));
-            const int first = before + __builtin_amdgcn_readlane(sum - tiles, l);
+        const uint32_t total = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(sum), 63));
+        if (!found && static_cast<uint32_t>(tile) < before + total) {
+            const int l = __builtin_ctzll(__ballot(before + sum > static_cast<uint32_t>(tile)));
+            const int first = static_cast<int>(before) + __builtin_amdgcn_readlane(static_cast<int>(sum - tiles), l);
             out.group = base + l;
             out.begin = __builtin_amdgcn_readlane(lo, l);
             out.m0 = out.begin + (tile - first) * bm;
             out.end = __builtin_amdgcn_readlane(hi, l);
-            found = true;
             if (!count) return true;
+            found = true;
         }
-        before += total;
+        before = min(before + total, kMostTiles);
     }
-    if (count) *count = before;
-    return found;
+    if (count) *count = static_cast<int>(before);
+    return found && tile >= 0;
 }
 
 // Position of block `bid` among `total` that are dealt out so that each XCD
