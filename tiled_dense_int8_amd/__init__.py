@@ -434,6 +434,8 @@ def _empty(like, shape, dtype, stream):
     """A new tensor of the stream that the call runs on (so that its memory
     is not handed out again while the call still runs)."""
     if stream is None:
+        if like.shape == shape and like.is_contiguous():
+            return torch.empty_like(like, dtype=dtype)  # the cheapest of torch's ways
         return like.new_empty(shape, dtype=dtype)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)

@@ -55,6 +55,11 @@ struct Operand<F8> {
     static __device__ __forceinline__ f32x4 mma(const Operand &b, const Operand &a) {
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
     }
+    static __device__ __forceinline__ void add(const Operand &b, const Operand &a, float scale, f32x4 &acc) {
+        const f32x4 part = mma(b, a);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], scale, acc[e]);
+    }
 };
 template <>
 struct Operand<F8Wide> {
@@ -68,6 +73,22 @@ struct Operand<F8Wide> {
 #pragma unroll
         for (int h = 0; h < 4; ++h) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[h], a.v[h], part, 0, 0, 0);
         return part;
+    }
+    static __device__ __forceinline__ void add(const Operand &b, const Operand &a, float scale, f32x4 &acc) {
+        const f32x4 part = mma(b, a);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], scale, acc[e]);
+    }
+};
+template <>
+struct Operand<S8> {
+    i32x8 v;
+    __device__ __forceinline__ void set(i32x8 pieces) { v = pieces; }
+    static __device__ __forceinline__ void add(const Operand &b, const Operand &a, float, i32x4 &acc) {
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{b.v[0], b.v[1], b.v[2], b.v[3]},
+                                                    i32x4{a.v[0], a.v[1], a.v[2], a.v[3]}, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{b.v[4], b.v[5], b.v[6], b.v[7]},
+                                                    i32x4{a.v[4], a.v[5], a.v[6], a.v[7]}, acc, 0, 0, 0);
     }
 };
 

@@ -34,7 +34,7 @@ constexpr LdsTile kF8WideTile[kLdsTiles] = {{64, 128, 256, 1, 7.0f, 20.0f},
                                             {128, 128, 256, 2, 10.0f, 55.0f},
                                             {}};
 // Tile of the kernel for unaligned operands (staged_product.h).
-constexpr LdsTile kStagedTile = {64, 128, 256, 1, 0.0f, 0.0f};
+constexpr LdsTile kStagedTile = {64, 128, 512, 1, 0.0f, 0.0f};
 
 struct ProductKernels {
     const void *stream[kStreamTiles][2];  // [tile][aligned]

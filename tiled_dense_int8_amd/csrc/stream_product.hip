@@ -21,7 +21,7 @@ static void register_stream(ProductKernels *k) {
 
 void TDI8_PRODUCT_REGISTER(ProductKernels *k) {
     register_stream<0>(k);
-    k->staged = reinterpret_cast<const void *>(&staged_product_kernel<TDI8_PRODUCT_TYPE, 2, 2, 2, 4>);
+    k->staged = reinterpret_cast<const void *>(&staged_product_kernel<TDI8_PRODUCT_TYPE, 2, 4, 2, 2>);
 }
 
 }  // namespace tdi8
