@@ -418,3 +418,58 @@ def test_dense_layer_f8():
     check_f8(up, want, H, torch.float16, "first product")
     want = f8_reference(q2.cpu(), sq2.cpu(), w2, s2)
     check_f8(out, want, I, torch.float32, "second product")
+
+
+# For each stream kernel a product that it is taken for: rows and columns that
+# end inside tiles, chunks of K that the waves share unevenly, a last one of 16
+# bytes (aligned operands) or of 77.
+STREAMED = [(5, 1999), (16, 4111), (30, 3999), (64, 3999), (128, 3999), (200, 3999)]
+UNALIGNED = [(3, 4201), (16, 1999), (13, 5001), (30, 1501), (60, 1501), (100, 999)]
+STREAM_CASES = [(M, N, 2832) for M, N in STREAMED] + [(M, N, 1101) for M, N in UNALIGNED]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("size", STREAM_CASES, ids=lambda s: "x".join(map(str, s)))
+def test_f8_streams(size, kind):
+    run_f8(gen(sum(size)), *size, kind, ld=(32, 16, 1), scale_pad=1)
+
+
+@pytest.mark.parametrize("size", STREAM_CASES, ids=lambda s: "x".join(map(str, s)))
+def test_grouped_streams(size):
+    """The same as one group, and shared by three of which one is empty."""
+    M, N, K = size
+    g = gen(sum(size))
+    run_grouped(g, [M], N, K, "bf16", T=M + 3, ld=(16, 0, 3))
+    run_grouped(g, [M // 2, 0, M - M // 2], N, K, "f32", T=M + 3)
+
+
+@pytest.mark.parametrize("counts", [[1] * 40, [3, 0, 20, 16], [0, 1, 2, 33, 8, 0, 1, 1]], ids=lambda c: f"{len(c)}x{max(c)}")
+def test_grouped_stream_of_few_rows(counts):
+    g = gen(max(counts))
+    for N, K in ((700, 2832), (699, 2832), (129, 112), (33, 4096)):
+        run_grouped(g, counts, N, K, "f16", slack=5)
+
+
+def test_streams_captured_together():
+    """Two stream products on one captured stream, replayed over changing inputs."""
+    g = gen(77)
+    A, B = e4m3(g, 24, 2832).cuda(), e4m3(g, 999, 2832).cuda()
+    sa, sb = scales(g, 24, 23).cuda(), scales(g, 8, 23).cuda()
+    A8, B8 = s8(g, 24, 1024).cuda(), s8(g, 3, 500, 1024).cuda()
+    ra, rb = scales(g, 24).cuda(), scales(g, 3, 500).cuda()
+    off = torch.tensor([0, 4, 4, 24], dtype=torch.int32).cuda()
+    y, z = torch.empty(24, 999, device="cuda"), torch.empty(24, 500, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        t.gemm_f8(A, sa, B, sb, out=y)
+        t.grouped_gemm(A8, ra, B8, rb, off, out=z)
+    for k in range(4):
+        A.copy_(e4m3(g, 24, 2832))
+        A8.copy_(s8(g, 24, 1024))
+        off.copy_(torch.tensor([0, 4 + k, 5 + k, 24], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, t.gemm_f8(A, sa, B, sb, dtype=torch.float32))
+        assert torch.equal(z, t.grouped_gemm(A8, ra, B8, rb, off, dtype=torch.float32))
+        check_f8(y, f8_reference(A.cpu(), sa.cpu(), B.cpu(), sb.cpu()), 2832, torch.float32, f"replay {k}")

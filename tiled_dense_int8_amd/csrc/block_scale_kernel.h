@@ -29,7 +29,7 @@
 // instruction whose part they add (kLag), across steps and tiles.
 #pragma once
 
-#include "stream_product.h"
+#include "operand_types.h"
 
 namespace tdi8 {
 

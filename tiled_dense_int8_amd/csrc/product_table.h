@@ -5,39 +5,53 @@
 
 namespace tdi8 {
 
-// Stream kernels (stream_product.h): block tile, waves sharing K, chunks that
-// a wave loads at once.
-enum { kStreamTiles = 6 };
-struct StreamTile {
-    int bm, bn, waves, batch;
-};
-constexpr StreamTile kStreamTile[kStreamTiles] = {
-    {16, 16, 4, 4}, {16, 16, 8, 4}, {16, 32, 4, 2}, {32, 16, 8, 2}, {32, 32, 4, 2}, {64, 32, 8, 1}};
-
-// Tiles of the kernels that stage both operands in LDS, and what they were
-// measured to take: a round of `per_cu` blocks on every compute unit costs
-// fixed + per_4096 * K / 4096 microseconds.
-struct LdsTile {
+// Tiles of a kernel, and what a product of them was measured to take: start
+// microseconds, and for each round of `per_cu` blocks on every compute unit
+// fixed + per_4096 * K / 4096.
+struct Tile {
     int bm, bn, threads;
     int per_cu;
-    float fixed, per_4096;
+    float start, fixed, per_4096;
 };
+
+// The kernels that stage both operands in LDS.
 enum { kLdsTiles = 4 };
-constexpr LdsTile kGroupedTile[kLdsTiles] = {
-    {64, 128, 512, 1, 2.5f, 14.0f}, {128, 256, 512, 1, 8.0f, 31.0f}, {256, 256, 512, 1, 12.0f, 58.0f}, {}};
-constexpr LdsTile kF8Tile[kLdsTiles] = {{64, 128, 256, 1, 6.0f, 16.0f},
-                                        {128, 128, 256, 1, 7.0f, 24.0f},
-                                        {128, 128, 256, 2, 9.0f, 34.0f},
-                                        {256, 256, 512, 1, 12.0f, 58.0f}};
-constexpr LdsTile kF8WideTile[kLdsTiles] = {{64, 128, 256, 1, 7.0f, 20.0f},
-                                            {128, 128, 256, 1, 8.0f, 34.0f},
-                                            {128, 128, 256, 2, 10.0f, 55.0f},
-                                            {}};
-// Tile of the kernel for unaligned operands (staged_product.h).
-constexpr LdsTile kStagedTile = {64, 128, 512, 1, 0.0f, 0.0f};
+constexpr Tile kGroupedTile[kLdsTiles] = {{64, 128, 512, 1, 0.0f, 2.5f, 14.0f},
+                                          {128, 256, 512, 1, 0.0f, 8.0f, 31.0f},
+                                          {256, 256, 512, 1, 0.0f, 12.0f, 58.0f},
+                                          {}};
+constexpr Tile kF8Tile[kLdsTiles] = {{64, 128, 256, 1, 0.0f, 6.0f, 16.0f},
+                                     {128, 128, 256, 1, 0.0f, 7.0f, 24.0f},
+                                     {128, 128, 256, 2, 0.0f, 9.0f, 34.0f},
+                                     {256, 256, 512, 1, 0.0f, 12.0f, 58.0f}};
+constexpr Tile kF8WideTile[kLdsTiles] = {{64, 128, 256, 1, 0.0f, 7.0f, 20.0f},
+                                         {128, 128, 256, 1, 0.0f, 8.0f, 34.0f},
+                                         {128, 128, 256, 2, 0.0f, 10.0f, 55.0f},
+                                         {}};
+
+// The stream kernels (stream_product.h); the types differ by less than the
+// steps from tile to tile.  The last one is for groups of few rows and chosen
+// by a rule of its own.
+enum { kStreamTiles = 7, kGroupStream = 6 };
+constexpr Tile kStreamTile[kStreamTiles] = {{8, 16, 512, 1, 3.0f, 0.1f, 1.75f},  {16, 16, 512, 1, 3.0f, 0.1f, 1.75f},
+                                            {32, 16, 512, 1, 2.9f, 0.2f, 2.45f}, {32, 32, 512, 1, 2.7f, 0.4f, 3.5f},
+                                            {32, 64, 512, 1, 1.5f, 1.9f, 5.3f},  {64, 64, 512, 1, 1.5f, 2.6f, 8.4f},
+                                            {16, 32, 256, 1, 0.0f, 0.0f, 0.0f}};
+
+// The kernels for unaligned operands: streams through registers
+// (unaligned_stream.h: block tile, waves sharing K, chunks that a wave loads at
+// once) and tiles staged in LDS (staged_product.h).
+enum { kUnalignedStreamTiles = 6 };
+struct UnalignedStreamTile {
+    int bm, bn, waves, batch;
+};
+constexpr UnalignedStreamTile kUnalignedStreamTile[kUnalignedStreamTiles] = {
+    {16, 16, 4, 4}, {16, 16, 8, 4}, {16, 32, 4, 2}, {32, 16, 8, 2}, {32, 32, 4, 2}, {64, 32, 8, 1}};
+enum { kStagedRows = 64, kStagedColumns = 128, kStagedThreads = 512 };
 
 struct ProductKernels {
-    const void *stream[kStreamTiles][2];  // [tile][aligned]
+    const void *stream[kStreamTiles];
+    const void *unaligned_stream[kUnalignedStreamTiles];
     const void *staged;
 };
 void register_products_s8(ProductKernels *k);

@@ -1,95 +1,41 @@
-// Products of few rows, and of operands that the tile kernels cannot load
-// (rows or K off 16-byte alignment): every wave streams its share of K
-// straight from memory into registers.
+// Products of few rows: every wave streams its share of K.
 //
-// Block: 16 MT rows of one group, 16 NT columns, all of K, which its W waves
-// share by chunks of 128 (wave w takes chunks w, w + W, ...).  With few rows
-// the product is a stream over B, read once: there are N / (16 NT) blocks per
-// group, enough to keep every compute unit's loads in flight, and no byte of
-// B passes through LDS, since no two waves want the same one.
+// Block: BM rows of one group, BN columns, all of K, which its W waves share by
+// chunks of 128 (wave w takes chunks w, w + W, ...).  A wave moves a chunk of
+// its BM + BN rows into LDS of its own by 16-byte LDS DMA, eight whole 128-byte
+// lines an instruction, reads it back as operands (operand_types.h), and sends
+// the next chunk's loads before it multiplies.  No wave waits for another
+// before the end, where the partial tiles are summed in the order of the waves
+// (a result does not depend on which came first).  Rows past the end repeat the
+// last one; of BM = 8 rows each is read by two lanes.
 //
-// Operands.  Lane l = 16 q + r holds, of row r of A and of column r of B, the
-// 16-byte pieces q and 4 + q of the chunk (one load instruction covers 64
-// contiguous bytes of 16 rows); both operands permute K alike, so the sum is
-// that of the chunk.  s8: two v_mfma_i32_16x16x64_i8 a chunk.  e4m3: one
-// v_mfma_f32_16x16x128_f8f6f4, whose 128 products of K are exactly a scale
-// block, then acc += scale * part in fp32 (for fp32 results see F8Wide).  B is
-// the first operand and A the second, so a lane ends with four consecutive
-// columns of one row.
-//
-// The waves' partial tiles are summed in LDS in the order of the waves, so a
-// result does not depend on which came first.
+// With few rows the product is a read of B, bound by HBM: 16 x 65536 x 4096
+// e4m3 51.4 us, 5.2 TB/s; 16 x 4096 x 4096 5.9 us, of which 3 are a launch's.
+// Through the middle (64 to 512 rows) a block's (BM + BN) K bytes from L2 bound
+// it, about 31 bytes a cycle and compute unit; the larger tiles read less, the
+// smaller fill the chip, and the choice weighs the two by their measured costs
+// (product_table.h; 256 x 4096 x 4096 e4m3: 13.9 us at 64 x 64, 19.9 at
+// 32 x 32, 22 with the LDS tiles; 64 x 4096 x 4096: 14.3, 8.1 and 21.8).
+// Two or four chunks of LDS a wave instead of one: 16 x 4096 x 4096 5.9 and
+// 6.0 us, 64 x 4096 x 4096 9.2, so what lies beside the other blocks of the
+// compute unit counts for more.
 #pragma once
 
-#include "scaled_product.h"
+#include "block_scale_kernel.h"
 
 namespace tdi8 {
 
-struct S8 {
-    using Acc = i32x4;
-    static constexpr bool kBlockScales = false;
-    static __device__ __forceinline__ void chunk(const i32x4 (&a)[2], const i32x4 (&b)[2], float, Acc &acc) {
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[0], a[0], acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[1], a[1], acc, 0, 0, 0);
-    }
-};
-// The e4m3 instructions add the 16 products of a 16-byte piece after cutting
-// each to a multiple of 2^-13 of the largest one's power of two (measured:
-// 2^5 + 2^-8 is exact within a piece, 2^6 + 2^-8 gives 2^6; between pieces
-// sums are fp32).  On normal operands a result is off by 1.5 * 10^-5 of the
-// results' size, far below half a step of the 16-bit types (2^-9, 2^-12).
-struct F8 {
-    using Acc = f32x4;
-    static constexpr bool kBlockScales = true;
-    static __device__ __forceinline__ i32x8 join(const i32x4 (&v)[2]) {
-        return i32x8{v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
-    }
-    static __device__ __forceinline__ void chunk(const i32x4 (&a)[2], const i32x4 (&b)[2], float scale, Acc &acc) {
-        // scale arguments of 0 select the instruction without block exponents
-        const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(b), join(a), f32x4{0, 0, 0, 0}, 0, 0,
-                                                                            0, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], scale, acc[e]);
-    }
-};
-
-// For fp32 results: e4m3 widened to bf16 (exact), whose products are added in
-// fp32: v_mfma_f32_16x16x32_bf16, four a chunk, at half the rate.
-struct F8Wide {
-    using Acc = f32x4;
-    static constexpr bool kBlockScales = true;
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-    static __device__ __forceinline__ bf16x8 widen(int32_t lo, int32_t hi) {
-        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-        return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-    }
-    static __device__ __forceinline__ void chunk(const i32x4 (&a)[2], const i32x4 (&b)[2], float scale, Acc &acc) {
-        f32x4 part = {0, 0, 0, 0};
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const i32x4 x = b[h >> 1], y = a[h >> 1];
-            const int o = 2 * (h & 1);
-            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(x[o], x[o + 1]), widen(y[o], y[o + 1]), part, 0, 0, 0);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], scale, acc[e]);
-    }
-};
-
-constexpr int kChunk = 128;
-
-// ALIGNED: A, B, lda, ldb, group_b and K are multiples of 16.
-template <class E, int MT, int NT, int W, int U, bool ALIGNED>
+template <class E, int BM, int BN, int W>
 __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
+    constexpr int MT = (BM + 15) / 16, NT = BN / 16;
+    constexpr int PIECES = (BM + BN) / 8;
+    constexpr int SCALES = (BM + BN) * kChunk;
+    constexpr int STAGE = SCALES + (E::kBlockScales ? 256 : 0);
+    static_assert(16 * MT * BN * 4 <= STAGE && W * STAGE <= 160 * 1024, "LDS");
+    static_assert(BM <= 64, "one load takes a chunk's scales");
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int BM = 16 * MT, BN = 16 * NT;
-    constexpr int RS = BN + 4;  // row stride of a partial tile in LDS
     using Acc = typename E::Acc;
-    __shared__ __attribute__((aligned(16))) Acc part[W * BM * RS / 4];
+    __shared__ __attribute__((aligned(1024))) int8_t lds[W * STAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, q = lane >> 4;
@@ -103,87 +49,122 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
     if (!find_rows(g, BM, static_cast<int>(at - static_cast<int64_t>(tn) * g.tiles_m), rt, nullptr)) return;
     const int n0 = tn * BN;
 
-    const int8_t *pa[MT], *pb[NT];
-    const float *psa[MT];
+    // rows past the group repeat its last one; rows outside A are zeroed at the end
+    auto row_a = [&](int r) { return g.A + max(a_row(g, min(rt.m0 + r, rt.end - 1)), 0) * g.lda; };
+    auto row_b = [&](int r) {
+        return g.B + rt.group * g.group_b + static_cast<int64_t>(min(n0 + r, g.N - 1)) * g.ldb;
+    };
+    // Load i fills LDS rows 8 i .. 8 i + 7 of a stage, A's and then B's.
+    const int lrow = lane >> 3;
+    const int8_t *src[PIECES];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int m = min(rt.m0 + 16 * i + r16, rt.end - 1);  // rows past the group repeat its last one
-        const int r = max(a_row(g, m), 0);                    // rows outside A are zeroed at the end
-        pa[i] = g.A + r * g.lda;
-        psa[i] = g.a_scale + (E::kBlockScales ? r * g.ldas : 0);
+    for (int i = 0; i < PIECES; ++i) {
+        const int r = 8 * i + lrow - (8 * i < BM ? 0 : BM);
+        src[i] = (8 * i < BM ? row_a(r) : row_b(r)) + wave * kChunk + 16 * ((lane & 7) ^ row16_swizzle(r & 15));
     }
+    const float *ssrc = nullptr, *psb = nullptr;
+    if constexpr (E::kBlockScales) {
+        ssrc = g.a_scale + min(rt.m0 + lane % BM, rt.end - 1) * g.ldas + wave;
+        psb = g.b_scale + (n0 / kChunk) * g.ldbs + wave;  // 128 is a multiple of BN
+    }
+    int8_t *const mine = lds + wave * STAGE;
+    const int whole = g.K / kChunk;
+    const int n = whole > wave ? (whole - wave + W - 1) / W : 0;
+    // A block that reads its part of B alone starts at a chunk of its own: rows
+    // a power of two apart lie in one memory channel, which all blocks would
+    // want at once (1 x 32768 x 4096 e4m3 27.7 -> 23.7 us, 8 groups of 2 rows,
+    // 11008 x 4096 int8 75 -> 65; 2 groups, 4096 x 4096, whose B the cache still
+    // holds, 8.0 -> 9.1).  Blocks that share B stay in step.
+    const int turn = n > 0 && rt.end - rt.begin <= BM ? static_cast<int>(blockIdx.x >> 3) % n : 0;
+    auto turned = [&](int c) { return c + turn < n ? c + turn : c + turn - n; };
+    auto issue = [&](int c) {
+        c = turned(c);
+        if constexpr (E::kBlockScales)
+            __builtin_amdgcn_global_load_lds(ssrc + c * W, (lds_void_t *)(mine + SCALES), 4, 0, 0);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-        pb[j] = g.B + rt.group * g.group_b + static_cast<int64_t>(min(n0 + 16 * j + r16, g.N - 1)) * g.ldb;
-    const float *psb = E::kBlockScales ? g.b_scale + (n0 / kChunk) * g.ldbs : nullptr;  // 128 is a multiple of BN
+        for (int i = 0; i < PIECES; ++i)
+            __builtin_amdgcn_global_load_lds(src[i] + c * (W * kChunk), (lds_void_t *)(mine + 1024 * i), 16, 0, 0);
+    };
 
     Acc acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = Acc{};
-
-    auto load = [&](const int8_t *p, int k, auto whole) -> i32x4 {
-        if constexpr (decltype(whole)::value)
-            return ALIGNED ? load16(p + k) : load16_unaligned(p + k);
-        else
-            return load16_masked(p + k, clamp16(g.K - k));
-    };
-    const int whole = g.K / kChunk;
-    // U chunks a time, all of their loads before the first product: a wave has
-    // U (MT + NT) KiB on the way at once.
-    auto chunks = [&](int kc, auto count, auto whole) {
-        constexpr int C = decltype(count)::value;
-        i32x4 a[C][MT][2], b[C][NT][2];
-        float s[C][MT];
+    const int ra = r16 % BM;
+    const int lo_a = ra * kChunk + 16 * (q ^ row16_swizzle(ra));
+    const int lo_b = (BM + r16) * kChunk + 16 * (q ^ row16_swizzle(r16));
+    if (n > 0) issue(0);
+    for (int c = 0; c < n; ++c) {
+        const float scale_b = E::kBlockScales ? psb[turned(c) * W] : 0.0f;
+        TDI8_WAIT_VMCNT(0);
+        asm volatile("" ::: "memory");
+        i32x4 a[MT][2], b[NT][2];
+        float s[MT];
 #pragma unroll
-        for (int u = 0; u < C; ++u) {
-            const int k = (kc + u * W) * kChunk + 16 * q;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                b[u][j][0] = load(pb[j], k, whole);
-                b[u][j][1] = load(pb[j], k + 64, whole);
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                a[u][i][0] = load(pa[i], k, whole);
-                a[u][i][1] = load(pa[i], k + 64, whole);
-                s[u][i] = E::kBlockScales ? psa[i][kc + u * W] * psb[kc + u * W] : 0.0f;
-            }
+        for (int i = 0; i < MT; ++i) {
+            a[i][0] = load16(mine + i * 2048 + lo_a);
+            a[i][1] = load16(mine + i * 2048 + (lo_a ^ 64));
+            s[i] = E::kBlockScales ? *reinterpret_cast<const float *>(mine + SCALES + 64 * i + 4 * ra) : 0.0f;
         }
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < C; ++u)
+        for (int j = 0; j < NT; ++j) {
+            b[j][0] = load16(mine + j * 2048 + lo_b);
+            b[j][1] = load16(mine + j * 2048 + (lo_b ^ 64));
+        }
+        if (c + 1 < n) {
+            TDI8_WAIT_LGKM0();  // the chunk is in registers
+            asm volatile("" ::: "memory");
+            issue(c + 1);
+        }
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) E::chunk(a[u][i], b[u][j], s[u][i], acc[i][j]);
-    };
-    using One = std::integral_constant<int, 1>;
-    int kc = wave;
-    if constexpr (U > 1)
-        for (; kc + (U - 1) * W < whole; kc += U * W) chunks(kc, std::integral_constant<int, U>{}, std::true_type{});
-    for (; kc < whole; kc += W) chunks(kc, One{}, std::true_type{});
-    if (whole * kChunk < g.K && whole % W == wave) chunks(whole, One{}, std::false_type{});
+            for (int j = 0; j < NT; ++j) E::chunk(a[i], b[j], s[i] * scale_b, acc[i][j]);
+    }
+    if (whole * kChunk < g.K && whole % W == wave) {  // the last, partial chunk
+        const int k = whole * kChunk + 16 * q;
+        i32x4 b[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                b[j][h] = load16_masked(row_b(16 * j + r16) + k + 64 * h, clamp16(g.K - k - 64 * h));
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            i32x4 a[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                a[h] = load16_masked(row_a(16 * i + r16) + k + 64 * h, clamp16(g.K - k - 64 * h));
+            float s = 0.0f;
+            if constexpr (E::kBlockScales)
+                s = g.a_scale[min(rt.m0 + 16 * i + r16, rt.end - 1) * g.ldas + whole] * psb[whole - wave];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) E::chunk(a, b[j], s, acc[i][j]);
+        }
+    }
 
     // partial tiles: a lane writes four consecutive columns of its row
+    constexpr int PART = STAGE / 16;  // from one wave's to the next
+    Acc *part = reinterpret_cast<Acc *>(lds);
+    auto at_part = [](int r, int c4) { return r * (BN / 4) + (c4 ^ (r & (BN / 4 - 1))); };
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            part[((wave * BM + 16 * i + r16) * RS + 16 * j) / 4 + q] = acc[i][j];
+            part[wave * PART + at_part(16 * i + r16, 4 * j + q)] = acc[i][j];
     __syncthreads();
     for (int x = threadIdx.x; x < BM * (BN / 4); x += W * 64) {
-        const int r = x / (BN / 4), c = x - r * (BN / 4);
-        const int m = rt.m0 + r, n = n0 + 4 * c;
-        if (m >= rt.end || n >= g.N) continue;
-        Acc sum = part[r * RS / 4 + c];
+        const int r = x / (BN / 4), c4 = x - r * (BN / 4);
+        const int m = rt.m0 + r, nn = n0 + 4 * c4;
+        if (m >= rt.end || nn >= g.N) continue;
+        Acc sum = part[at_part(r, c4)];
 #pragma unroll
-        for (int w = 1; w < W; ++w) sum += part[(w * BM + r) * RS / 4 + c];
+        for (int w = 1; w < W; ++w) sum += part[w * PART + at_part(r, c4)];
         if constexpr (E::kBlockScales)
-            store_row4(g, m, n, sum);
+            store_row4(g, m, nn, sum);
         else
-            store_scaled4(g, rt.group, rt.end, m, n, sum);
+            store_scaled4(g, rt.group, rt.end, m, nn, sum);
     }
 #endif
 }
