@@ -27,70 +27,22 @@
 // soon as both steps are done with it, so the next tile starts with operands
 // in place.  Scaled additions follow three instructions behind the matrix
 // instruction whose part they add (kLag), across steps and tiles.
+//
+// Measured on MI355X: 4096^3 to bf16 72 to 77 us (1.8 PFLOP/s), 8192^3 500 to
+// 550 us (2.1 PFLOP/s; the range is that of the chip's clock from one machine
+// to the next; a plain e4m3 product of that size without scales reaches 2.6),
+// to fp32 4096^3 129 us.  At 8192^3 the matrix cores are busy 57% of the
+// cycles at 1.63 GHz, the clock that power allows; LDS reads and DMA writes
+// take as many cycles as the matrix work beside them ((128 + 64) rows read for
+// 128 x 64 results a wave; wider wave tiles need more accumulators than a
+// wave has registers that multiply-adds can address).  Tiles: 256 x 256 of two
+// stages for many rows; 128 x 128 twice on a compute unit, or with four
+// stages once; 64 x 128 with four (product_table.h has their costs).
 #pragma once
 
 #include "operand_types.h"
 
 namespace tdi8 {
-
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-// Permutation of the 16-byte chunks of row r (128 bytes) for reads of 16 rows
-// by four chunks.  Such a read runs in four passes; measured by bank conflicts,
-// the first takes lanes 0-3, 12-15, 20-23 and 24-27, the second 4-11, 16-19 and
-// 28-31, the others the same 32 lanes on: rows 0-3 and 12-15 at one chunk with
-// rows 4-11 at the next.  Even rows lie in one half of the 256 bytes of all
-// banks, odd ones in the other, so the eight even (odd) ones of a pass must get
-// different chunks: c ^ (r & 2 | 4 (r / 8 & 1)) gives {0, 2, 4, 6} and {1, 3, 5, 7}.
-// (chunk_swizzle, which suits reads of 32 rows, met itself twice in every pass.)
-__device__ __forceinline__ int row16_swizzle(int r) { return (r & 2) | (r >> 1 & 4); }
-
-// One operand of 16 rows x 128, as the instructions take it.
-template <class E>
-struct Operand;
-template <>
-struct Operand<F8> {
-    i32x8 v;
-    __device__ __forceinline__ void set(i32x8 pieces) { v = pieces; }
-    static __device__ __forceinline__ f32x4 mma(const Operand &b, const Operand &a) {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-    }
-    static __device__ __forceinline__ void add(const Operand &b, const Operand &a, float scale, f32x4 &acc) {
-        const f32x4 part = mma(b, a);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], scale, acc[e]);
-    }
-};
-template <>
-struct Operand<F8Wide> {
-    F8Wide::bf16x8 v[4];
-    __device__ __forceinline__ void set(i32x8 pieces) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) v[h] = F8Wide::widen(pieces[2 * h], pieces[2 * h + 1]);
-    }
-    static __device__ __forceinline__ f32x4 mma(const Operand &b, const Operand &a) {
-        f32x4 part = {0, 0, 0, 0};
-#pragma unroll
-        for (int h = 0; h < 4; ++h) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[h], a.v[h], part, 0, 0, 0);
-        return part;
-    }
-    static __device__ __forceinline__ void add(const Operand &b, const Operand &a, float scale, f32x4 &acc) {
-        const f32x4 part = mma(b, a);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], scale, acc[e]);
-    }
-};
-template <>
-struct Operand<S8> {
-    i32x8 v;
-    __device__ __forceinline__ void set(i32x8 pieces) { v = pieces; }
-    static __device__ __forceinline__ void add(const Operand &b, const Operand &a, float, i32x4 &acc) {
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{b.v[0], b.v[1], b.v[2], b.v[3]},
-                                                    i32x4{a.v[0], a.v[1], a.v[2], a.v[3]}, acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{b.v[4], b.v[5], b.v[6], b.v[7]},
-                                                    i32x4{a.v[4], a.v[5], a.v[6], a.v[7]}, acc, 0, 0, 0);
-    }
-};
 
 template <class E, int WM, int WN, int MT, int NT, int STAGES>
 __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArgs g) {
@@ -189,7 +141,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
 
     constexpr int RING = 4;  // A operands in registers: read two steps ahead
     constexpr int kLag = 3;  // scaled additions behind
-    i32x8 ra[RING];
+    i32x4 ra[RING][2];
     float rs[RING];
     Operand<E> ob[NT];
     float s[RING];           // a_scale * b_scale of the last steps
@@ -197,14 +149,13 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
     Operand<E> oa[RING];
     auto read_a = [&](int kt, int i) {
         const int8_t *p = lds + (kt & (STAGES - 1)) * STAGE;
-        const i32x4 lo = piece(p + lo_a + i * (16 * BK)), hi = piece(p + (lo_a ^ 64) + i * (16 * BK));
-        ra[i % RING] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        ra[i % RING][0] = piece(p + lo_a + i * (16 * BK));
+        ra[i % RING][1] = piece(p + (lo_a ^ 64) + i * (16 * BK));
         rs[i % RING] = *reinterpret_cast<const float *>(p + ls + i * 64);
     };
     auto read_b = [&](int kt, int j) {
         const int8_t *p = lds + (kt & (STAGES - 1)) * STAGE;
-        const i32x4 lo = piece(p + lo_b + j * (16 * BK)), hi = piece(p + (lo_b ^ 64) + j * (16 * BK));
-        ob[j].set(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        ob[j].set(piece(p + lo_b + j * (16 * BK)), piece(p + (lo_b ^ 64) + j * (16 * BK)));
     };
     // Matrix instruction x of a tile works on step step_of(x), column col_of(x):
     // row by row, the last two steps column by column.
@@ -266,7 +217,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) block_scale_kernel(ProductArg
                     if constexpr (LOAD) issue(kt + STAGES);
                 }
                 if constexpr (x < TAIL && j == 0) read_a(kt, i + 2);
-                if constexpr (j == 0) oa[i % RING].set(ra[i % RING]);
+                if constexpr (j == 0) oa[i % RING].set(ra[i % RING][0], ra[i % RING][1]);
                 part[x % (kLag + 1)] = Operand<E>::mma(ob[j], oa[i % RING]);
                 add(x - kLag);
                 // The scales of a step, before its first addition and, for the

@@ -30,9 +30,10 @@
 //
 // Measured on MI355X (bytes read and written once over the time; a device
 // copy of 1 GiB runs at 5.2 TB/s): norm of 16384 x 8192 bf16 with a residual
-// 162 us (5.8 TB/s) s8, 160 us f8; 4096 x 16384 89 us (5.3 TB/s); 2048 x 20000,
+// 162 us (5.8 TB/s) s8, 163 us f8; 4096 x 16384 89 us (5.3 TB/s); 2048 x 20000,
 // read twice, 94 us (3.1 TB/s).  act of 8192 x 11008 bf16 118 us (3.8 TB/s)
-// s8, 106 us (4.3 TB/s) f8: there the exponential's instructions count.
+// s8, 100 us (4.5 TB/s) f8: there the exponential's instructions count.  A
+// single row of 4096 columns takes 3 us, most of it the launch.
 #pragma once
 
 #include "quant_rows.h"

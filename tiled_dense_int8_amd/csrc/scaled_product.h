@@ -9,6 +9,7 @@ namespace tdi8 {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void_t;
 
 struct ProductArgs {
     const int8_t *A, *B;  // int8 or e4m3 bytes, K contiguous

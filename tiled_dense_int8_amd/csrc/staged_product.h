@@ -20,7 +20,7 @@
 // and 27.9.
 #pragma once
 
-#include "block_scale_kernel.h"
+#include "operand_types.h"
 
 namespace tdi8 {
 
@@ -102,9 +102,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) staged_product_kernel(Product
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = Acc{};
     const int sw = row16_swizzle(r16);
-    auto read = [&](const int8_t *p, int r) {
-        const i32x4 lo = load16(p + r * BK + 16 * (q ^ sw)), hi = load16(p + r * BK + 16 * ((q + 4) ^ sw));
-        return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    auto read = [&](Operand<E> &o, const int8_t *p, int r) {
+        o.set(load16(p + r * BK + 16 * (q ^ sw)), load16(p + r * BK + 16 * ((q + 4) ^ sw)));
     };
     if (nk > 0) fetch(0);
     for (int kt = 0; kt < nk; ++kt) {
@@ -116,12 +115,12 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) staged_product_kernel(Product
         const int8_t *p = lds + (kt & 1) * STAGE;
         Operand<E> b[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) b[j].set(read(p, BM + wn * (NT * 16) + j * 16 + r16));
+        for (int j = 0; j < NT; ++j) read(b[j], p, BM + wn * (NT * 16) + j * 16 + r16);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int r = wm * (MT * 16) + i * 16 + r16;
             Operand<E> a;
-            a.set(read(p, r));
+            read(a, p, r);
             const float s = E::kBlockScales ? *reinterpret_cast<const float *>(p + SCALES + 4 * r) * scale_b : 0.0f;
 #pragma unroll
             for (int j = 0; j < NT; ++j) Operand<E>::add(b[j], a, s, acc[i][j]);

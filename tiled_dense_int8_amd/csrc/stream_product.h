@@ -21,7 +21,7 @@
 // compute unit counts for more.
 #pragma once
 
-#include "block_scale_kernel.h"
+#include "operand_types.h"
 
 namespace tdi8 {
 
@@ -117,30 +117,34 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
             asm volatile("" ::: "memory");
             issue(c + 1);
         }
+        Operand<E> ob[NT], oa;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int j = 0; j < NT; ++j) ob[j].set(b[j][0], b[j][1]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) E::chunk(a[i], b[j], s[i] * scale_b, acc[i][j]);
+        for (int i = 0; i < MT; ++i) {
+            oa.set(a[i][0], a[i][1]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) Operand<E>::add(ob[j], oa, s[i] * scale_b, acc[i][j]);
+        }
     }
     if (whole * kChunk < g.K && whole % W == wave) {  // the last, partial chunk
         const int k = whole * kChunk + 16 * q;
-        i32x4 b[NT][2];
+        auto load = [&](const int8_t *p, int h) { return load16_masked(p + k + h, clamp16(g.K - k - h)); };
+        Operand<E> ob[NT], oa;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                b[j][h] = load16_masked(row_b(16 * j + r16) + k + 64 * h, clamp16(g.K - k - 64 * h));
+        for (int j = 0; j < NT; ++j) {
+            const int8_t *p = row_b(16 * j + r16);
+            ob[j].set(load(p, 0), load(p, 64));
+        }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            i32x4 a[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                a[h] = load16_masked(row_a(16 * i + r16) + k + 64 * h, clamp16(g.K - k - 64 * h));
+            const int8_t *p = row_a(16 * i + r16);
+            oa.set(load(p, 0), load(p, 64));
             float s = 0.0f;
             if constexpr (E::kBlockScales)
                 s = g.a_scale[min(rt.m0 + 16 * i + r16, rt.end - 1) * g.ldas + whole] * psb[whole - wave];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) E::chunk(a, b[j], s, acc[i][j]);
+            for (int j = 0; j < NT; ++j) Operand<E>::add(ob[j], oa, s, acc[i][j]);
         }
     }
 

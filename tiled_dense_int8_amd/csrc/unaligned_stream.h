@@ -85,11 +85,17 @@ __global__ void __launch_bounds__(W * 64) unaligned_stream_kernel(ProductArgs g)
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < C; ++u)
+        for (int u = 0; u < C; ++u) {
+            Operand<E> ob[NT], oa;
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int j = 0; j < NT; ++j) ob[j].set(b[u][j][0], b[u][j][1]);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) E::chunk(a[u][i], b[u][j], s[u][i], acc[i][j]);
+            for (int i = 0; i < MT; ++i) {
+                oa.set(a[u][i][0], a[u][i][1]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) Operand<E>::add(ob[j], oa, s[u][i], acc[i][j]);
+            }
+        }
     };
     using One = std::integral_constant<int, 1>;
     int kc = wave;
