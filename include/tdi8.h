@@ -351,7 +351,8 @@ int conv2d_validate(int N, int H, int W, int C, int K, int R, int S,
  *   f8  8-bit floating point (e4m3: 4 exponent and 3 mantissa bits, largest
  *       value 448, no infinity) with one scale per row and block of 128
  *       columns (the last block may be shorter): scale = max|y| / 448.
- * q is exact: the integer (e4m3 value) nearest to the real quotient, ties to
+ * q is exact: the integer nearest to the real quotient, or the e4m3 value
+ * nearest to its 32-bit form (as a conversion from 32 bits gives it), ties to
  * even, whatever the order of the sums: values next to a border between two
  * are decided in 64 bits.  s8 scales are computed in 64 bits and rounded once;
  * f8 scales of the activation, and of the norm of 32-bit values, come from the

@@ -55,7 +55,8 @@ def quantise(v, inv, fmt):
 
 
 def e4m3_nearest(t):
-    """64-bit values up to 448 rounded to e4m3 (3 mantissa bits, exponents from -6 on), ties to even."""
+    """64-bit values up to 448 rounded to fp32 and then to e4m3 (3 mantissa bits, exponents from -6 on), ties to even."""
+    t = t.float().double()
     _, exponent = torch.frexp(t)  # t = f * 2^exponent, 1/2 <= |f| < 1
     step = torch.exp2(((exponent - 1).clamp(min=-6) - 3).double())
     return torch.round(t / step) * step
@@ -64,8 +65,8 @@ def e4m3_nearest(t):
 def check_quantised(q, scale, v, inv, fmt, what, steps=10):
     """q and scale against the quotients in 64 bits.
 
-    q: equal to the integer, or e4m3 value, nearest to the quotient, ties to
-    even.  scale: computed in 64 bits and rounded once to fp32, half a step =
+    q: equal to the integer nearest to the quotient, or the e4m3 value nearest
+    to its fp32 form, ties to even.  scale: computed in 64 bits and rounded once to fp32, half a step =
     2^-24 relative (values in fp32's normal range), plus what two 64-bit
     computations differ by (< 2^-40).  f8: a block's largest value may be a
     32-bit one, off by `steps` times 2^-24: 10 for the activation, 1 for the

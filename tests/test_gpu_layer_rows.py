@@ -252,3 +252,26 @@ def test_more_rows_than_a_grid_holds():
     q, scale = t.swiglu(x, x, fmt="f8")
     assert torch.equal(q.float(), (448 * torch.sign(x * x)))
     assert scale.shape == (T, 1) and scale[-1] > 0 and scale.isfinite().all()
+
+
+def test_f8_quotients_next_to_a_border_go_by_their_fp32_form():
+    """Quotients above a border between two e4m3 values by less than 2^-25 of it count as on it: ties to even."""
+    H, columns = 128, []
+    for border, below in ((17.0, 16.0), (19.0, 20.0), (1.0625 * 256, 256.0), (2.125, 2.0)):  # and what its tie gives
+        for i in range(1, 4000):
+            w = 1 + i * 2.0 ** -23
+            h = torch.tensor(border * (1 + 2.0 ** -22) / w, dtype=torch.float64).float().item()
+            # v = h w in whole units of 2^-60: above the border's v = border (1 + 2^-22)?
+            v = int(h * 2.0 ** 30) * int(w * 2.0 ** 30)
+            at = int(border * 2.0 ** 30) * (2 ** 30 + 2 ** 8)
+            if h * 2.0 ** 30 == int(h * 2.0 ** 30) and 0 < v - at < at >> 26:
+                columns.append((h, w, below))
+                if len(columns) % 20 == 0:
+                    break
+    assert len(columns) == 80
+    x, weight, want = torch.zeros(1, H), torch.ones(H), torch.zeros(H)
+    x[0, 0], weight[0], want[0] = 448.0, 1 + 2.0 ** -22, 448.0
+    for k, (h, w, q) in enumerate(columns):
+        x[0, 1 + k], weight[1 + k], want[1 + k] = h, w, q
+    q, _ = t.rms_norm(x.cuda(), weight.cuda(), fmt="f8")
+    assert torch.equal(q.float().cpu()[0], want)

@@ -9,14 +9,15 @@
 //         q = e4m3(448 v / max|v|)
 //
 // The norm's root cancels out of q, so q needs the row's (block's) largest
-// |v| only and the root goes into the scale.  q is exact: the integer or e4m3
-// value nearest to the real quotient, ties to even.  The quotient is first
-// taken in fp32 with a known error (kNear, kOff); where it lies that near a
-// border between two values it is taken again in fp64.  Without this, values
-// next to a border would round by the last bit of a sum or an exponential, and
-// two orders of the same computation would give different bytes.  The sum of
-// squares is held in fp64: finite inputs cannot overflow it, and it then says
-// whether a row holds an infinity or NaN.
+// |v| only and the root goes into the scale.  q is exact: the integer nearest
+// to the real quotient, or the e4m3 value nearest to the real quotient rounded
+// to fp32, ties to even.  The quotient is first taken in fp32 with a known
+// error (kNear, kOff); where it lies that near a border between two values it
+// is taken again in fp64.  Without this, values next to a border would round by
+// the last bit of a sum or an exponential, and two orders of the same
+// computation would give different bytes.  The sum of squares is held in fp64:
+// finite inputs cannot overflow it, and it then says whether a row holds an
+// infinity or NaN.
 //
 // A row (f8: block) that holds an infinity or NaN has q = 0 and scale = NaN,
 // so that products with it come out NaN; one of zeros has q = 0 and scale = 0.
@@ -291,14 +292,10 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
 }
-// x as an e4m3 byte.  The fp32 value between is rounded to odd (towards zero,
-// the last bit set where anything was lost), so that the second rounding sees
-// on which side of a border x lies.
+// x as an e4m3 byte, by way of fp32: the same byte as a conversion of the fp32
+// quotient gives (a quotient within 2^-25 of a border counts as on it).
 __device__ __forceinline__ uint32_t e4m3_of(double x) {
-    float f = static_cast<float>(x);
-    if (fabs(static_cast<double>(f)) > fabs(x)) f = __uint_as_float(__float_as_uint(f) - 1u);
-    if (static_cast<double>(f) != x) f = __uint_as_float(__float_as_uint(f) | 1u);
-    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(f, 0.0f, 0, false)) & 0xffu;
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(static_cast<float>(x), 0.0f, 0, false)) & 0xffu;
 }
 
 // fp32 values from 2^22 up to 2^23 in magnitude plus this have their integer
