@@ -1,0 +1,186 @@
+"""The layer operators' ordinary calls (module _calls) against the calls by Python, and what each refuses."""
+import sys
+
+import pytest
+import torch
+
+import tiled_dense_int8_amd as t
+
+pytestmark = pytest.mark.gpu
+F8 = torch.float8_e4m3fn
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def normal(g, *shape, dtype=torch.bfloat16):
+    return torch.randn(*shape, generator=g).to(dtype).cuda()
+
+
+def s8(g, *shape):
+    return torch.randint(-128, 128, shape, generator=g, dtype=torch.int8).cuda()
+
+
+def scales(g, *shape):
+    return (torch.rand(*shape, generator=g) + 0.1).cuda()
+
+
+def same(a, b):
+    a, b = (x if isinstance(x, tuple) else (x,) for x in (a, b))
+    assert len(a) == len(b)
+    for x, y in zip(a, b):
+        assert x.dtype == y.dtype and x.shape == y.shape and x.stride() == y.stride() and x.device == y.device
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def where():
+    device = torch.cuda.current_device()
+    return device, torch.cuda.current_stream().cuda_stream
+
+
+def native(name, *args):
+    """The call through _calls alone (None where it leaves the call to Python)."""
+    return getattr(t._calls, name)(*args, *where())
+
+
+@pytest.mark.parametrize("fmt", ["s8", "f8"])
+@pytest.mark.parametrize("shape", [(0, 5), (1, 1), (1, 4096), (7, 130), (33, 1000)])
+def test_rows_alike(shape, fmt):
+    g = gen(sum(shape))
+    stream = torch.cuda.current_stream()
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        x, r, w = normal(g, *shape, dtype=dtype), normal(g, *shape, dtype=dtype), normal(g, shape[1], dtype=dtype)
+        got = native("rms_norm", x, w, 1e-5, r, fmt, None, None, None)
+        assert got is not None
+        same(got, t.rms_norm(x, w, 1e-5, residual=r, fmt=fmt, stream=stream))
+        same(t.rms_norm(x, w, 1e-5, fmt=fmt), t.rms_norm(x, w, 1e-5, fmt=fmt, stream=stream))
+        assert native("swiglu", x, r, fmt, None, None) is not None
+        same(t.swiglu(x, r, fmt=fmt), t.swiglu(x, r, fmt=fmt, stream=stream))
+        both = torch.cat((x, r), 1)
+        same(t.swiglu(both[:, :shape[1]], both[:, shape[1]:], fmt=fmt), t.swiglu(x, r, fmt=fmt, stream=stream))
+    torch.cuda.synchronize()
+
+
+def test_products_alike():
+    g = gen(3)
+    stream = torch.cuda.current_stream()
+    for M, N, K in ((1, 1, 1), (3, 40, 128), (20, 300, 777), (70, 129, 256)):
+        kb, nb = -(-K // 128), -(-N // 128)
+        A, B = (normal(g, *s, dtype=torch.float32).to(F8) for s in ((M, K), (N, K)))
+        sa, sb = scales(g, M, kb), scales(g, nb, kb)
+        A8, B8, ra, rb = s8(g, M, K), s8(g, 2, N, K), scales(g, M), scales(g, 2, N)
+        off = torch.tensor([0, M // 2, M], dtype=torch.int32).cuda()
+        rows = torch.randint(0, M, (M,), generator=g, dtype=torch.int32).cuda()
+        for dtype in (torch.float32, torch.bfloat16, torch.float16):
+            assert native("gemm_f8", A, sa, B, sb, None, dtype) is not None
+            same(t.gemm_f8(A, sa, B, sb, dtype=dtype), t.gemm_f8(A, sa, B, sb, dtype=dtype, stream=stream))
+            for o, r in ((off, rows), (off, None)):
+                assert native("grouped_gemm", A8, ra, B8, rb, o, r, None, dtype) is not None
+                same(t.grouped_gemm(A8, ra, B8, rb, o, rows=r, dtype=dtype),
+                     t.grouped_gemm(A8, ra, B8, rb, o, rows=r, dtype=dtype, stream=stream))
+            assert native("grouped_gemm", A8, ra, B8[0], rb[0], None, None, None, dtype) is not None
+            same(t.grouped_gemm(A8, ra, B8[0], rb[0], dtype=dtype),
+                 t.grouped_gemm(A8, ra, B8[:1], rb[:1], rows=None, dtype=dtype, stream=stream))
+    torch.cuda.synchronize()
+
+
+def test_outputs_of_the_caller():
+    """Given outputs are the ones returned, written in place, and no reference is kept."""
+    g = gen(4)
+    x, r, w = normal(g, 5, 300), normal(g, 5, 300), normal(g, 300)
+    want = t.rms_norm(x, w, residual=r, fmt="f8")
+    out, scale, total = (torch.empty(5, 320, dtype=F8).cuda()[:, :300], torch.empty(5, 3).cuda(), r.clone())
+    before = [sys.getrefcount(o) for o in (x, out, scale, total)]
+    for _ in range(3):
+        total.copy_(r)
+        got = t.rms_norm(x, w, residual=total, fmt="f8", sum_out=total, out=out, scale=scale)
+        assert got[0] is out and got[1] is scale and got[2] is total
+        for a, b in zip(got, want):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.view(torch.uint8))
+        del got, a
+    assert [sys.getrefcount(o) for o in (x, out, scale, total)] == before
+    A8, B8, ra, rb = s8(g, 4, 64), s8(g, 1, 30, 64), scales(g, 4), scales(g, 1, 30)
+    y = torch.empty(4, 32).cuda()[:, :30]
+    assert t.grouped_gemm(A8, ra, B8, rb, out=y) is y
+    assert torch.equal(y, t.grouped_gemm(A8, ra, B8, rb, dtype=torch.float32))
+    q = torch.empty(5, 300, dtype=torch.int8).cuda()
+    assert t.swiglu(x, r, out=q)[0] is q
+
+
+def test_left_to_python():
+    """Calls that _calls does not make work all the same, or are refused by name."""
+    g = gen(5)
+    x, w = normal(g, 5, 300), normal(g, 300)
+    want = t.rms_norm(x, w, 0.0)
+    for eps in (0, torch.tensor(0.0)):  # not a Python float
+        assert native("rms_norm", x, w, eps, None, "s8", None, None, None) is None
+    same(t.rms_norm(x, w, 0), want)
+    same(t.rms_norm(x, torch.nn.Parameter(w), 0.0), want)
+    same(t.rms_norm(x.as_subclass(type("Mine", (torch.Tensor,), {})), w, 0.0), want)
+    A, B, sa, sb = (normal(g, 4, 256, dtype=torch.float32).to(F8), normal(g, 30, 256, dtype=torch.float32).to(F8),
+                    scales(g, 4, 2), scales(g, 1, 2))
+    A8, B8, ra, rb = s8(g, 4, 64), s8(g, 2, 30, 64), scales(g, 4), scales(g, 2, 30)
+    off = torch.tensor([0, 1, 4], dtype=torch.int32).cuda()
+    refused = [
+        (TypeError, lambda: t.rms_norm(x.double(), w)), (ValueError, lambda: t.rms_norm(x, w.float())),
+        (ValueError, lambda: t.rms_norm(x, w[1:])), (ValueError, lambda: t.rms_norm(x.t(), w[:5])),
+        (ValueError, lambda: t.rms_norm(x, w, fmt="int8")), (ValueError, lambda: t.rms_norm(x, w, sum_out=x)),
+        (ValueError, lambda: t.rms_norm(x, w.cpu())), (TypeError, lambda: t.rms_norm(x, w, residual=x.float())),
+        (ValueError, lambda: t.rms_norm(x[0], w)), (TypeError, lambda: t.rms_norm(x, w, out=torch.empty(5, 300).cuda())),
+        (ValueError, lambda: t.rms_norm(x, w, scale=torch.empty(4).cuda())),
+        (ValueError, lambda: t.swiglu(x, x[:4])), (ValueError, lambda: t.swiglu(x[:1].expand(5, 300), x)),
+        (TypeError, lambda: t.gemm_f8(A.view(torch.int8), sa, B, sb)), (ValueError, lambda: t.gemm_f8(A, sa[:, :1], B, sb)),
+        (ValueError, lambda: t.gemm_f8(A[:, :128], sa[:, :1], B, sb)), (TypeError, lambda: t.gemm_f8(A, sa, B, sb, dtype=torch.int8)),
+        (ValueError, lambda: t.gemm_f8(A, sa, B, sb, out=torch.empty(4, 31).cuda())),
+        (ValueError, lambda: t.grouped_gemm(A8, ra, B8, rb)), (ValueError, lambda: t.grouped_gemm(A8, ra, B8, rb, off[:2])),
+        (ValueError, lambda: t.grouped_gemm(A8, ra, B8, rb, off.long())),
+        (ValueError, lambda: t.grouped_gemm(A8, ra, B8, rb[:, ::2], off)),
+        (ValueError, lambda: t.grouped_gemm(A8, ra[:3], B8, rb, off)),
+        (TypeError, lambda: t.grouped_gemm(A8, ra, B8.float(), rb, off)),
+    ]
+    for k, (error, call) in enumerate(refused):
+        with pytest.raises(error):
+            call()
+            print("not refused:", k)
+
+
+def test_status_becomes_an_error():
+    g = gen(6)
+    A, sa = normal(g, 64, 128, dtype=torch.float32).to(F8), scales(g, 64, 1)
+    with pytest.raises(t.TDI8Error) as e:
+        t.gemm_f8(A, sa, A, scales(g, 1, 1), out=A.view(torch.float16))
+    assert e.value.status == t.ERR_ALIASING
+    x = normal(g, 4, 64)
+    for call in (lambda: t.rms_norm(x, x[0], float("nan")), lambda: t.rms_norm(x, x[0], -1.0)):
+        with pytest.raises(t.TDI8Error) as e:
+            call()
+        assert e.value.status == t.ERR_INVALID_VALUE
+    x8 = torch.zeros(4, 64, dtype=torch.int8).cuda()
+    with pytest.raises(t.TDI8Error):
+        t.swiglu(x8.view(torch.float16), x8.view(torch.float16), out=x8[:, :32])
+
+
+def test_other_streams_and_threads():
+    """The current stream is the one used, in threads of their own too."""
+    import threading
+    g = gen(7)
+    x, w = normal(g, 300, 4000), normal(g, 4000)
+    want = t.rms_norm(x, w, fmt="f8")
+    torch.cuda.synchronize()
+    results = {}
+
+    def work(k):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            y = x + 0
+            for _ in range(20):
+                results[k] = t.rms_norm(y, w, fmt="f8")
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    for k in range(4):
+        same(results[k], want)

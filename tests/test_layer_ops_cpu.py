@@ -165,3 +165,21 @@ def test_product_wrappers_refuse():
     for kw in dict(B=F[:, :128]), dict(a_scale=fs[:3]), dict(b_scale=gs[:, :1]), dict(a_scale=torch.zeros(2, 4).t()):
         with pytest.raises(ValueError):
             t.gemm_f8(**{**dict(A=F, a_scale=fs, B=F, b_scale=gs), **kw})
+
+
+def test_native_calls_leave_others_to_python():
+    """_calls makes no call it cannot: CPU tensors, other objects, other counts of arguments."""
+    x, w = torch.zeros(2, 8), torch.ones(8)
+    q = torch.zeros(2, 128).to(torch.float8_e4m3fn)
+    s = torch.ones(2, 1)
+    i8 = torch.zeros(2, 8, dtype=torch.int8)
+    for name, args in (("rms_norm", (x, w, 1e-6, None, "s8", None, None, None)), ("swiglu", (x, x, "s8", None, None)),
+                       ("gemm_f8", (q, s, q, s[:1], None, torch.float32)),
+                       ("grouped_gemm", (i8, w[:2], i8, w[:2], None, None, None, torch.float32))):
+        call = getattr(t._calls, name)
+        assert call(*args, 0, 0) is None
+        assert call(*args) is None and call() is None
+        assert call(*args, None, "stream") is None
+        for k in range(len(args)):
+            for other in (None, 3, "x", [1], object()):
+                assert call(*args[:k], other, *args[k + 1:], 0, 0) is None

@@ -5,8 +5,8 @@ HIP kernels (C ABI in include/tdi8.h).  The names mirror the C entry points;
 ``gemm`` is a convenience wrapper that takes torch tensors, whose only role
 is device memory and the current stream.
 
-There is no fallback: if libtdi8.so is missing or fails to load, importing
-this package raises.  Build it with ``python tiled_dense_int8_amd/build.py``
+There is no fallback: if libtdi8.so or the module _calls is missing or fails to
+load, importing this package raises.  Build it with ``python tiled_dense_int8_amd/build.py``
 (or ``__graft_entry__.build()``).
 """
 from __future__ import annotations
@@ -21,7 +21,10 @@ LIB_PATH = os.path.join(_HERE, "libtdi8.so")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with tiled_dense_int8_amd/build.py")
+if not os.path.exists(os.path.join(_HERE, "_calls.so")):
+    raise ImportError(f"{_HERE}/_calls.so is missing: build it with tiled_dense_int8_amd/build.py")
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _calls  # noqa: E402
 
 OK = 0
 ERR_INVALID_VALUE = -1
@@ -380,7 +383,12 @@ def swiglu_quant_f8(type, T, N, gate, ldg, up, ldu, q, ldq, scale, lds, stream=0
 
 
 # The wrappers below are called for single tokens, where their own time is what
-# counts: they look at each tensor once and call the library directly.
+# counts.  Calls with dense tensors on the current device and no stream named go
+# through _calls (csrc/calls.cpp), which checks the same things natively; it
+# returns None for all others, which the Python below makes or refuses.
+_calls.bind(TDI8Error, *(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
+    "rmsnorm_quant_s8", "rmsnorm_quant_f8", "swiglu_quant_s8", "swiglu_quant_f8", "gemm_s8s8_grouped",
+    "gemm_f8f8_block128")))
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -481,6 +489,11 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, fmt: str = "s8", sum_o
        (T, ceil(H / 128)), one for each block of 128 columns.
     sum_out: where the sum goes (x or residual itself: in place).
     """
+    if stream is None and x.is_cuda:
+        device = _current_device()
+        made = _calls.rms_norm(x, weight, eps, residual, fmt, sum_out, out, scale, device, _current_stream(device))
+        if made is not None:
+            return made
     dtype = x.dtype
     code = _TYPES.get(dtype)
     if code is None:
@@ -512,6 +525,11 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, fmt: str = "s8", sum_o
 def swiglu(gate, up, fmt: str = "s8", out=None, scale=None, stream=None):
     """(q, scale) of gate / (1 + exp(-gate)) * up for gate and up (T, N), in
     the formats of rms_norm; the two may be halves of one tensor's rows."""
+    if stream is None and gate.is_cuda:
+        device = _current_device()
+        made = _calls.swiglu(gate, up, fmt, out, scale, device, _current_stream(device))
+        if made is not None:
+            return made
     dtype = gate.dtype
     code = _TYPES.get(dtype)
     if code is None:
@@ -570,6 +588,11 @@ def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtyp
     out: (M, N) of a floating type, or dtype for a new tensor; rows from
        offsets[G] on are not written.
     """
+    if stream is None and A.is_cuda:
+        device = _current_device()
+        made = _calls.grouped_gemm(A, a_scale, B, b_scale, offsets, rows, out, dtype, device, _current_stream(device))
+        if made is not None:
+            return made
     lda = _matrix("A", A, torch.int8)
     T, K = A.shape
     if B.dtype != torch.int8:
@@ -609,6 +632,11 @@ def gemm_f8(A, a_scale, B, b_scale, out=None, dtype=torch.bfloat16, stream=None)
     B: float8_e4m3fn (N, K), b_scale: float32 (ceil(N / 128), ceil(K / 128)).
     out: (M, N) of a floating type, or dtype for a new tensor.
     """
+    if stream is None and A.is_cuda:
+        device = _current_device()
+        made = _calls.gemm_f8(A, a_scale, B, b_scale, out, dtype, device, _current_stream(device))
+        if made is not None:
+            return made
     lda = _matrix("A", A, torch.float8_e4m3fn)
     ldb = _matrix("B", B, torch.float8_e4m3fn)
     (M, K), N = A.shape, B.shape[0]

@@ -14,16 +14,20 @@ carries the SHA-256 of those code objects (tdi8_kernel_code_hash).
 The library build also produces libtdi8_ceilings.so (roofline calibration
 kernels) and libtdi8_stamps.so: the same sources compiled with TDI8_STAMPS,
 whose kernels write per-block timelines (include/tdi8_stamps.h); its
-objects go to _build/stamps/.
+objects go to _build/stamps/.  _calls.so is the Python module of the 8-bit
+layer operators' ordinary calls (csrc/calls.cpp), host code against torch's
+headers.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import hashlib
+import importlib.util
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 import yaml
 
@@ -34,8 +38,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtdi8.so")
 CEILINGS_LIB = os.path.join(PKG, "libtdi8_ceilings.so")  # roofline calibration kernels (bench.py --ceilings)
+CALLS_LIB = os.path.join(PKG, "_calls.so")                 # ordinary calls of the layer operators
 STAMPS_LIB = os.path.join(PKG, "libtdi8_stamps.so")      # block timelines (bench.py --stamps)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 LLVM_BIN = "/opt/rocm/llvm/bin"
 ARCH = "gfx950"
 
@@ -131,6 +137,16 @@ def write_resource_table(objs: dict[int, str], bdir: str) -> str:
     return src
 
 
+def calls_unit(out: str) -> list[str]:
+    """The command that builds the Python module _calls (host code)."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    include = os.path.join(torch_dir, "include")
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-I", INCLUDE,
+            "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.cpp"),
+            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", out]
+
+
 def build(jobs: int | None = None, verbose: bool = False, extra_flags: list[str] | None = None,
           out: str | None = None, build_dir: str | None = None) -> str:
     """Compile every configuration and link the library (default: in-tree libtdi8.so)."""
@@ -164,7 +180,8 @@ def build(jobs: int | None = None, verbose: bool = False, extra_flags: list[str]
     ceil_obj = os.path.join(bdir, "ceilings.o")
     ceil_unit = [HIPCC, *flags, "-c", os.path.join(CSRC, "ceilings.hip"), "-o", ceil_obj]
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        list(ex.map(_run, units + ([ceil_unit] if out == LIB else [])))
+        calls_tmp = CALLS_LIB + ".tmp%d" % os.getpid()
+        list(ex.map(_run, ([calls_unit(calls_tmp), ceil_unit] if out == LIB else []) + units))
     objs = [u[u.index("-o") + 1] for u in units]
     res_src = write_resource_table({cid: os.path.join(bdir, f"cfg{cid}.o") for cid in config_ids()}, bdir)
     res_obj = os.path.join(bdir, "kernel_resources.o")
@@ -174,6 +191,7 @@ def build(jobs: int | None = None, verbose: bool = False, extra_flags: list[str]
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp])
     os.replace(tmp, out)
     if out == LIB:
+        os.replace(calls_tmp, CALLS_LIB)
         tmp = CEILINGS_LIB + ".tmp%d" % os.getpid()
         _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", ceil_obj, "-o", tmp])
         os.replace(tmp, CEILINGS_LIB)
