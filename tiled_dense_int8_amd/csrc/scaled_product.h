@@ -147,16 +147,28 @@ __device__ __forceinline__ void store_row4(const ProductArgs &g, int64_t m, int 
     }
 }
 
-// Four sums of int8 products of row m (below `end`) from column n on, scaled.
-__device__ __forceinline__ void store_scaled4(const ProductArgs &g, int group, int end, int m, int n, i32x4 sum) {
-    if (m >= end || n >= g.N) return;
-    const int row = a_row(g, m);
-    const float sa = row < 0 ? 0.0f : g.a_scale[row];
-    const float *sb = g.b_scale + static_cast<int64_t>(group) * g.N;
+// Scales of four results of a row of an int8 product, from column n on.  Read
+// before the sums are made: at the end the row's index, its scale and the store
+// would wait for each other (8 groups of 1000 rows, 1501 x 777: 14.6 us against
+// 13.2; 16 of 1024, 512 x 2048: 10.5 and 9.6).
+struct Scales4 {
+    int row;  // of A, or -1: zeros
+    float a;
+    f32x4 b;
+};
+__device__ __forceinline__ Scales4 load_scales4(const ProductArgs &g, const RowTile &rt, int m, int n) {
+    Scales4 s;
+    s.row = a_row(g, min(m, rt.end - 1));
+    s.a = g.a_scale[max(s.row, 0)];
+    const float *sb = g.b_scale + static_cast<int64_t>(rt.group) * g.N;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s.b[e] = sb[min(n + e, g.N - 1)];
+    return s;
+}
+__device__ __forceinline__ void store_scaled4(const ProductArgs &g, int m, int n, i32x4 sum, const Scales4 &s) {
     f32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        v[e] = row < 0 ? 0.0f : static_cast<float>(sum[e]) * (sa * sb[min(n + e, g.N - 1)]);
+    for (int e = 0; e < 4; ++e) v[e] = s.row < 0 ? 0.0f : static_cast<float>(sum[e]) * (s.a * s.b[e]);
     store_row4(g, m, n, v);
 }
 

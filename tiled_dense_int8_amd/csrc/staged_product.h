@@ -32,6 +32,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) staged_product_kernel(Product
     constexpr int LOADS = (BM + BN) * CPR / THREADS;
     constexpr int SCALES = (BM + BN) * BK;
     constexpr int STAGE = SCALES + (E::kBlockScales ? BM * 4 : 0);
+    constexpr int RS = BN + 4, ITEMS = BM * (BN / 4) / THREADS;  // of four results a thread
+    static_assert(BM * (BN / 4) % THREADS == 0 && BM * RS * 4 <= 2 * STAGE, "C fits the stages");
     static_assert((BM + BN) * CPR % THREADS == 0 && BM <= THREADS, "loads split evenly");
     static_assert(128 % (NT * 16) == 0 && BN % 128 == 0, "a wave's columns lie in one block of 128");
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -106,6 +108,14 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) staged_product_kernel(Product
         o.set(load16(p + r * BK + 16 * (q ^ sw)), load16(p + r * BK + 16 * ((q + 4) ^ sw)));
     };
     if (nk > 0) fetch(0);
+    Scales4 scales[ITEMS];
+    if constexpr (!E::kBlockScales) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int x = threadIdx.x + i * THREADS;
+            scales[i] = load_scales4(g, rt, rt.m0 + x / (BN / 4), n0 + x % (BN / 4) * 4);
+        }
+    }
     for (int kt = 0; kt < nk; ++kt) {
         stash(kt);
         const float scale_b = E::kBlockScales ? sb[kt] : 0.0f;
@@ -127,30 +137,26 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) staged_product_kernel(Product
         }
     }
 
-    // C through LDS in passes of 64 rows.
-    constexpr int RS = BN + 4, RP = 64;
-    static_assert(RP * RS * 4 <= 2 * STAGE, "a pass fits the stages");
+    // C through LDS
     Acc *cl = reinterpret_cast<Acc *>(lds);
-    for (int p0 = 0; p0 < BM; p0 += RP) {
-        __syncthreads();
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int rb = wm * (MT * 16) + i * 16;
-            if (rb < p0 || rb >= p0 + RP) continue;
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) cl[((rb - p0 + r16) * RS + wn * (NT * 16) + j * 16) / 4 + q] = acc[i][j];
-        }
-        __syncthreads();
-        for (int x = threadIdx.x; x < RP * (BN / 4); x += THREADS) {
-            const int r = x / (BN / 4), c = x - r * (BN / 4);
-            const int m = rt.m0 + p0 + r, n = n0 + 4 * c;
-            if (m >= rt.end || n >= g.N) continue;
-            const Acc v = cl[r * RS / 4 + c];
-            if constexpr (E::kBlockScales)
-                store_row4(g, m, n, v);
-            else
-                store_scaled4(g, rt.group, rt.end, m, n, v);
-        }
+        for (int j = 0; j < NT; ++j)
+            cl[((wm * (MT * 16) + i * 16 + r16) * RS + wn * (NT * 16) + j * 16) / 4 + q] = acc[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int x = threadIdx.x + i * THREADS;
+        const int r = x / (BN / 4), c = x - r * (BN / 4);
+        const int m = rt.m0 + r, n = n0 + 4 * c;
+        if (m >= rt.end || n >= g.N) continue;
+        const Acc v = cl[r * RS / 4 + c];
+        if constexpr (E::kBlockScales)
+            store_row4(g, m, n, v);
+        else
+            store_scaled4(g, m, n, v, scales[i]);
     }
 #endif
 }

@@ -95,6 +95,15 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
     const int lo_a = ra * kChunk + 16 * (q ^ row16_swizzle(ra));
     const int lo_b = (BM + r16) * kChunk + 16 * (q ^ row16_swizzle(r16));
     if (n > 0) issue(0);
+    constexpr int ITEMS = (BM * (BN / 4) + W * 64 - 1) / (W * 64);  // of four results a thread
+    Scales4 scales[ITEMS];
+    if constexpr (!E::kBlockScales) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int x = threadIdx.x + i * (W * 64);
+            scales[i] = load_scales4(g, rt, rt.m0 + x / (BN / 4), n0 + x % (BN / 4) * 4);
+        }
+    }
     for (int c = 0; c < n; ++c) {
         const float scale_b = E::kBlockScales ? psb[turned(c) * W] : 0.0f;
         TDI8_WAIT_VMCNT(0);
@@ -158,17 +167,19 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
         for (int j = 0; j < NT; ++j)
             part[wave * PART + at_part(16 * i + r16, 4 * j + q)] = acc[i][j];
     __syncthreads();
-    for (int x = threadIdx.x; x < BM * (BN / 4); x += W * 64) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int x = threadIdx.x + i * (W * 64);
         const int r = x / (BN / 4), c4 = x - r * (BN / 4);
         const int m = rt.m0 + r, nn = n0 + 4 * c4;
-        if (m >= rt.end || nn >= g.N) continue;
+        if (x >= BM * (BN / 4) || m >= rt.end || nn >= g.N) continue;
         Acc sum = part[at_part(r, c4)];
 #pragma unroll
         for (int w = 1; w < W; ++w) sum += part[w * PART + at_part(r, c4)];
         if constexpr (E::kBlockScales)
             store_row4(g, m, nn, sum);
         else
-            store_scaled4(g, rt.group, rt.end, m, nn, sum);
+            store_scaled4(g, m, nn, sum, scales[i]);
     }
 #endif
 }

@@ -55,6 +55,15 @@ __global__ void __launch_bounds__(W * 64) unaligned_stream_kernel(ProductArgs g)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = Acc{};
 
+    constexpr int ITEMS = (BM * (BN / 4) + W * 64 - 1) / (W * 64);  // of four results a thread
+    Scales4 scales[ITEMS];
+    if constexpr (!E::kBlockScales) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int x = threadIdx.x + i * (W * 64);
+            scales[i] = load_scales4(g, rt, rt.m0 + x / (BN / 4), n0 + x % (BN / 4) * 4);
+        }
+    }
     auto load = [&](const int8_t *p, int k, auto whole) -> i32x4 {
         if constexpr (decltype(whole)::value)
             return load16_unaligned(p + k);
@@ -111,17 +120,19 @@ __global__ void __launch_bounds__(W * 64) unaligned_stream_kernel(ProductArgs g)
         for (int j = 0; j < NT; ++j)
             part[((wave * BM + 16 * i + r16) * RS + 16 * j) / 4 + q] = acc[i][j];
     __syncthreads();
-    for (int x = threadIdx.x; x < BM * (BN / 4); x += W * 64) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int x = threadIdx.x + i * (W * 64);
         const int r = x / (BN / 4), c = x - r * (BN / 4);
         const int m = rt.m0 + r, n = n0 + 4 * c;
-        if (m >= rt.end || n >= g.N) continue;
+        if (x >= BM * (BN / 4) || m >= rt.end || n >= g.N) continue;
         Acc sum = part[r * RS / 4 + c];
 #pragma unroll
         for (int w = 1; w < W; ++w) sum += part[(w * BM + r) * RS / 4 + c];
         if constexpr (E::kBlockScales)
             store_row4(g, m, n, sum);
         else
-            store_scaled4(g, rt.group, rt.end, m, n, sum);
+            store_scaled4(g, m, n, sum, scales[i]);
     }
 #endif
 }
