@@ -424,7 +424,7 @@ def test_dense_layer_f8():
 # end inside tiles, chunks of K that the waves share unevenly, a last one of 16
 # bytes (aligned operands) or of 77.
 STREAMED = [(5, 1999), (16, 4111), (30, 3999), (64, 3999), (128, 3999), (200, 3999)]
-UNALIGNED = [(3, 4201), (16, 1999), (13, 5001), (30, 1501), (60, 1501), (100, 999)]
+UNALIGNED = [(3, 4201), (16, 1999), (13, 5001), (30, 1501), (60, 1501), (100, 999), (150, 1501), (270, 1501)]
 STREAM_CASES = [(M, N, 2832) for M, N in STREAMED] + [(M, N, 1101) for M, N in UNALIGNED]
 
 

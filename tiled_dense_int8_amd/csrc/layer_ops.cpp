@@ -243,37 +243,19 @@ int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
     const ProductKernels &pk = *product_kernels(f8, g.type);
     const void *kernel = nullptr;
     int bm = 0, bn = 0, threads = 0;
-    auto take = [&](const void *k, int m, int n, int t) {
+    auto take = [&](const void *k, const Tile &t) {
         kernel = k;
-        bm = m;
-        bn = n;
-        threads = t;
+        bm = t.bm;
+        bn = t.bn;
+        threads = t.threads;
     };
     const int64_t lds = expected(64, 128);
-    if (!al) {
-        // Streams through registers: few tiles for the chip, or so few rows
-        // that B is read once anyway.
-        if (3 * lds < units || rows <= 1 || (groups == 1 && rows <= 16 && lds < units)) {
-            // One block of 16 columns for each compute unit or less: more
-            // waves a block.  More blocks: fewer waves, and 32 columns where
-            // the rows differ, which halves what is read of A.
-            int i = rows <= 16 ? 2 : rows <= 32 ? 3 : rows <= 64 ? 4 : 5;
-            if (i == 2 && expected(16, 16) <= units)
-                i = 1;
-            else if (i == 2 && groups == 1 && rows <= 4)
-                i = 0;
-            const UnalignedStreamTile &t = kUnalignedStreamTile[i];
-            take(pk.unaligned_stream[i], t.bm, t.bn, 64 * t.waves);
-        } else {
-            take(pk.staged, kStagedRows, kStagedColumns, kStagedThreads);
-        }
-    } else if (groups > 1 && (rows <= 2 || (rows <= 32 && lds < units))) {
+    if (groups > 1 && (rows <= 2 || (rows <= 32 && lds < units))) {
         // Groups of few rows: most row tiles hold few, so that B is read once
         // (int8: 256 groups of 2 rows on average, 1024 x 2048: 86 us, by LDS
         // tiles 118; 64 of 2, 2048 x 4096: 85 and 78; 8 of 16, 1024 x 4096: 10.4
         // and 18.8; 8 of 8, 4096 x 4096, where many have two row tiles: 33 and 27.6).
-        const Tile &t = kStreamTile[kGroupStream];
-        take(pk.stream[kGroupStream], t.bm, t.bn, t.threads);
+        take(al ? pk.stream[kGroupStream] : pk.unaligned_group, kStreamTile[kGroupStream]);
     } else {
         // the least of the tiles' measured costs; equal ones to the first
         float best = 0.0f;
@@ -283,19 +265,21 @@ int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
             const float cost = t.start + rounds * (t.fixed + t.per_4096 * g.K / 4096.0f);
             if (kernel && cost >= best) return;
             best = cost;
-            take(k, t.bm, t.bn, t.threads);
+            take(k, t);
         };
         // Streams while the LDS tiles leave compute units idle (512 x 4096 x
         // 4096 e4m3, 256 of those: 25 us against 22) or where B is all there is
         // to read (8 x 32768 x 4096: 25 against 28.6); no tile of twice the rows.
+        const Tile *streams = al ? kStreamTile : kUnalignedTile;
         if (lds < units || rows <= 8)
-            for (int i = 0; i < kGroupStream; ++i)
-                if (kStreamTile[i].bm < 2 * rows || i == 0) weigh(pk.stream[i], kStreamTile[i]);
-        if (near) {
+            for (int i = 0; i < (al ? +kGroupStream : +kUnalignedStreams); ++i)
+                if (streams[i].bm < 2 * rows || i == 0) weigh(al ? pk.stream[i] : pk.unaligned[i], streams[i]);
+        if (al && near) {
             const TileSet &set = tile_set(f8, g.type);
             for (int i = 0; i < kLdsTiles && set.kernel[i]; ++i) weigh(set.kernel[i], set.tile[i]);
+        } else {
+            for (const Tile &t : kStagedTile) weigh(pk.staged, t);
         }
-        if (!kernel) take(pk.staged, kStagedRows, kStagedColumns, kStagedThreads);
     }
     // every group that has rows ends in at most one partial tile
     const int64_t tm = (g.M + groups * (bm - 1)) / bm;

@@ -23,6 +23,27 @@ constexpr int kChunk = 128;
 // (chunk_swizzle, which suits reads of 32 rows, met itself twice in every pass.)
 __device__ __forceinline__ int row16_swizzle(int r) { return (r & 2) | (r >> 1 & 4); }
 
+// Bytes s .. s + 15 (0 <= s < 16) of the 32 in lo and hi.
+__device__ __forceinline__ i32x4 funnel16(i32x4 lo, i32x4 hi, int s) {
+    // (whole vectors, no array: that would be indexed in memory)
+    const bool two = (s & 8) != 0, one = (s & 4) != 0;
+    const i32x8 d = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    const i32x8 e = two ? i32x8{lo[2], lo[3], hi[0], hi[1], hi[2], hi[3], 0, 0} : d;
+    const i32x8 f = one ? i32x8{e[1], e[2], e[3], e[4], e[5], 0, 0, 0} : e;
+    i32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = static_cast<int32_t>(
+            __builtin_amdgcn_alignbyte(static_cast<uint32_t>(f[i + 1]), static_cast<uint32_t>(f[i]), s & 3));
+    return r;
+}
+// The first `n` bytes (any number; 16 and more: all), zeros behind them.
+__device__ __forceinline__ i32x4 keep16(i32x4 v, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = static_cast<int32_t>(keep_bytes(static_cast<uint32_t>(v[i]), n - 4 * i));
+    return v;
+}
+
 struct S8 {
     using Acc = i32x4;
     static constexpr bool kBlockScales = false;

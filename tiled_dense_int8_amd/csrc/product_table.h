@@ -38,20 +38,20 @@ constexpr Tile kStreamTile[kStreamTiles] = {{8, 16, 512, 1, 3.0f, 0.1f, 1.75f}, 
                                             {32, 64, 512, 1, 1.5f, 1.9f, 5.3f},  {64, 64, 512, 1, 1.5f, 2.6f, 8.4f},
                                             {16, 32, 256, 1, 0.0f, 0.0f, 0.0f}};
 
-// The kernels for unaligned operands: streams through registers
-// (unaligned_stream.h: block tile, waves sharing K, chunks that a wave loads at
-// once) and tiles staged in LDS (staged_product.h).
-enum { kUnalignedStreamTiles = 6 };
-struct UnalignedStreamTile {
-    int bm, bn, waves, batch;
-};
-constexpr UnalignedStreamTile kUnalignedStreamTile[kUnalignedStreamTiles] = {
-    {16, 16, 4, 4}, {16, 16, 8, 4}, {16, 32, 4, 2}, {32, 16, 8, 2}, {32, 32, 4, 2}, {64, 32, 8, 1}};
-enum { kStagedRows = 64, kStagedColumns = 128, kStagedThreads = 512 };
+// The kernels for unaligned operands: the streams of these tiles (64 x 64 has
+// too few registers for that), and tiles staged through registers
+// (staged_product.h; the same kernel with one block on a compute unit or two).
+enum { kUnalignedStreams = 5, kStagedTiles = 2 };
+constexpr Tile kUnalignedTile[kUnalignedStreams] = {{8, 16, 512, 1, 3.0f, 0.2f, 3.3f},
+                                                    {16, 16, 512, 1, 3.0f, 0.2f, 4.0f},
+                                                    {32, 16, 512, 1, 2.9f, 0.6f, 5.4f},
+                                                    {32, 32, 512, 1, 2.7f, 1.4f, 7.6f},
+                                                    {32, 64, 512, 1, 0.0f, 4.5f, 11.0f}};
+constexpr Tile kStagedTile[kStagedTiles] = {{64, 128, 512, 1, 0.0f, 2.2f, 46.0f}, {64, 128, 512, 2, 0.0f, 3.2f, 54.0f}};
 
 struct ProductKernels {
     const void *stream[kStreamTiles];
-    const void *unaligned_stream[kUnalignedStreamTiles];
+    const void *unaligned[kUnalignedStreams], *unaligned_group;
     const void *staged;
 };
 void register_products_s8(ProductKernels *k);

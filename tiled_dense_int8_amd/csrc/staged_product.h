@@ -4,8 +4,8 @@
 //
 // An unaligned 16-byte load runs at about a third of the rate of an aligned
 // one (21 of 58 bytes per cycle and compute unit from L2), so what counts is
-// how few of them a tile needs: a BM x BN tile loads BM + BN rows, where the
-// stream kernels' waves share nothing (1000 x 3000 x 777 e4m3: 33 us there).
+// how few of them a tile needs: a BM x BN tile loads BM + BN rows once, where
+// the stream kernels' tiles are smaller (1000 x 3000 x 777 e4m3: 24 us there).
 //
 // Two LDS stages, K tiles of 128.  A K tile's loads go out while the tile
 // before is multiplied, wait in registers and are written to the stage that

@@ -9,6 +9,14 @@
 // (a result does not depend on which came first).  Rows past the end repeat the
 // last one; of BM = 8 rows each is read by two lanes.
 //
+// Operands off 16-byte alignment (K, a pointer or a leading dimension): a chunk
+// of a row lies within nine aligned pieces, which go to LDS as they are (every
+// piece read holds a byte of the row); a lane shifts each pair of pieces that
+// it reads into place.  Unaligned loads into registers run at about a third of
+// the rate of aligned ones (21 of 58 bytes per cycle and compute unit from L2):
+// 16 x 4096 x 4095 e4m3 18.2 us by those, 8.0 by shifted pieces, 100 x 1000 x
+// 1001 8.9 and 4.6.
+//
 // With few rows the product is a read of B, bound by HBM: 16 x 65536 x 4096
 // e4m3 51.4 us, 5.2 TB/s; 16 x 4096 x 4096 5.9 us, of which 3 are a launch's.
 // Through the middle (64 to 512 rows) a block's (BM + BN) K bytes from L2 bound
@@ -18,18 +26,20 @@
 // 32 x 32, 22 with the LDS tiles; 64 x 4096 x 4096: 14.3, 8.1 and 21.8).
 // Two or four chunks of LDS a wave instead of one: 16 x 4096 x 4096 5.9 and
 // 6.0 us, 64 x 4096 x 4096 9.2, so what lies beside the other blocks of the
-// compute unit counts for more.
+// compute unit counts for more.  Loads into registers, 64 bytes of 16 rows an
+// instruction, ask for every line twice: 7.5 and 12.4 us.
 #pragma once
 
 #include "operand_types.h"
 
 namespace tdi8 {
 
-template <class E, int BM, int BN, int W>
+template <class E, int BM, int BN, int W, bool ALIGNED>
 __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
     constexpr int MT = (BM + 15) / 16, NT = BN / 16;
-    constexpr int PIECES = (BM + BN) / 8;
-    constexpr int SCALES = (BM + BN) * kChunk;
+    constexpr int PITCH = ALIGNED ? kChunk : kChunk + 16;  // of a row in LDS
+    constexpr int LOADS = ((BM + BN) * PITCH + 1023) / 1024;
+    constexpr int SCALES = LOADS * 1024;
     constexpr int STAGE = SCALES + (E::kBlockScales ? 256 : 0);
     static_assert(16 * MT * BN * 4 <= STAGE && W * STAGE <= 160 * 1024, "LDS");
     static_assert(BM <= 64, "one load takes a chunk's scales");
@@ -54,13 +64,16 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
     auto row_b = [&](int r) {
         return g.B + rt.group * g.group_b + static_cast<int64_t>(min(n0 + r, g.N - 1)) * g.ldb;
     };
-    // Load i fills LDS rows 8 i .. 8 i + 7 of a stage, A's and then B's.
-    const int lrow = lane >> 3;
-    const int8_t *src[PIECES];
+    // Load i fills the 1024 bytes i of a stage: A's rows and then B's.  Aligned,
+    // eight rows with their pieces permuted; otherwise the nine aligned pieces
+    // that hold a row's 128 bytes, for src, its bytes.
+    const int8_t *src[LOADS];
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-        const int r = 8 * i + lrow - (8 * i < BM ? 0 : BM);
-        src[i] = (8 * i < BM ? row_a(r) : row_b(r)) + wave * kChunk + 16 * ((lane & 7) ^ row16_swizzle(r & 15));
+    for (int i = 0; i < LOADS; ++i) {
+        const int x = 64 * i + lane;
+        const int row = x / (PITCH / 16), piece = x % (PITCH / 16);
+        const int r = row < BM ? row : row - BM;
+        src[i] = (row < BM ? row_a(r) : row_b(r)) + wave * kChunk + 16 * (ALIGNED ? piece ^ row16_swizzle(r & 15) : piece);
     }
     const float *ssrc = nullptr, *psb = nullptr;
     if constexpr (E::kBlockScales) {
@@ -69,7 +82,10 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
     }
     int8_t *const mine = lds + wave * STAGE;
     const int whole = g.K / kChunk;
-    const int n = whole > wave ? (whole - wave + W - 1) / W : 0;
+    const int some = ALIGNED ? whole : (g.K + kChunk - 1) / kChunk;  // chunks that take the loop
+    const int n = some > wave ? (some - wave + W - 1) / W : 0;
+    // bytes of chunk c of this wave
+    auto bytes = [&](int c) { return min(g.K - (wave + c * W) * kChunk, kChunk); };
     // A block that reads its part of B alone starts at a chunk of its own: rows
     // a power of two apart lie in one memory channel, which all blocks would
     // want at once (1 x 32768 x 4096 e4m3 27.7 -> 23.7 us, 8 groups of 2 rows,
@@ -82,8 +98,17 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
         if constexpr (E::kBlockScales)
             __builtin_amdgcn_global_load_lds(ssrc + c * W, (lds_void_t *)(mine + SCALES), 4, 0, 0);
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-            __builtin_amdgcn_global_load_lds(src[i] + c * (W * kChunk), (lds_void_t *)(mine + 1024 * i), 16, 0, 0);
+        for (int i = 0; i < LOADS; ++i) {
+            const int8_t *p = src[i] + c * (W * kChunk);
+            if constexpr (!ALIGNED) {
+                // the piece's first byte lies `over` behind the row's last of
+                // this chunk: load the last piece instead
+                const int s = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+                const int over = 16 * ((64 * i + lane) % (PITCH / 16)) - s - bytes(c);
+                p -= s + (over >= 0 ? (over & ~15) + 16 : 0);
+            }
+            __builtin_amdgcn_global_load_lds(p, (lds_void_t *)(mine + 1024 * i), 16, 0, 0);
+        }
     };
 
     Acc acc[MT][NT];
@@ -92,8 +117,27 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = Acc{};
     const int ra = r16 % BM;
-    const int lo_a = ra * kChunk + 16 * (q ^ row16_swizzle(ra));
-    const int lo_b = (BM + r16) * kChunk + 16 * (q ^ row16_swizzle(r16));
+    const int lo_a = ra * PITCH + 16 * (ALIGNED ? q ^ row16_swizzle(ra) : q);
+    const int lo_b = (BM + r16) * PITCH + 16 * (ALIGNED ? q ^ row16_swizzle(r16) : q);
+    int shift_a[MT], shift_b[NT];  // of the rows from 16 bytes
+    if constexpr (!ALIGNED) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            shift_a[i] = static_cast<int>(reinterpret_cast<uintptr_t>(row_a(16 * i + ra)) & 15);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            shift_b[j] = static_cast<int>(reinterpret_cast<uintptr_t>(row_b(16 * j + r16)) & 15);
+    }
+    // Pieces q and q + 4 of the row at p.
+    auto read = [&](const int8_t *p, int shift, i32x4 (&v)[2]) {
+        if constexpr (ALIGNED) {
+            v[0] = load16(p);
+            v[1] = load16(mine + ((p - mine) ^ 64));
+        } else {
+            v[0] = funnel16(load16(p), load16(p + 16), shift);
+            v[1] = funnel16(load16(p + 64), load16(p + 80), shift);
+        }
+    };
     if (n > 0) issue(0);
     constexpr int ITEMS = (BM * (BN / 4) + W * 64 - 1) / (W * 64);  // of four results a thread
     Scales4 scales[ITEMS];
@@ -112,19 +156,28 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
         float s[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            a[i][0] = load16(mine + i * 2048 + lo_a);
-            a[i][1] = load16(mine + i * 2048 + (lo_a ^ 64));
+            read(mine + i * (16 * PITCH) + lo_a, shift_a[i], a[i]);
             s[i] = E::kBlockScales ? *reinterpret_cast<const float *>(mine + SCALES + 64 * i + 4 * ra) : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            b[j][0] = load16(mine + j * 2048 + lo_b);
-            b[j][1] = load16(mine + j * 2048 + (lo_b ^ 64));
-        }
+        for (int j = 0; j < NT; ++j) read(mine + j * (16 * PITCH) + lo_b, shift_b[j], b[j]);
         if (c + 1 < n) {
             TDI8_WAIT_LGKM0();  // the chunk is in registers
             asm volatile("" ::: "memory");
             issue(c + 1);
+        }
+        if (!ALIGNED && bytes(turned(c)) < kChunk) {  // the last, partial chunk: zeros behind the rows' ends
+            const int left = bytes(turned(c)) - 16 * q;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                a[i][0] = keep16(a[i][0], left);
+                a[i][1] = keep16(a[i][1], left - 64);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                b[j][0] = keep16(b[j][0], left);
+                b[j][1] = keep16(b[j][1], left - 64);
+            }
         }
         Operand<E> ob[NT], oa;
 #pragma unroll
@@ -136,7 +189,7 @@ __global__ void __launch_bounds__(W * 64) stream_product_kernel(ProductArgs g) {
             for (int j = 0; j < NT; ++j) Operand<E>::add(ob[j], oa, s[i] * scale_b, acc[i][j]);
         }
     }
-    if (whole * kChunk < g.K && whole % W == wave) {  // the last, partial chunk
+    if (ALIGNED && whole * kChunk < g.K && whole % W == wave) {  // the last, partial chunk
         const int k = whole * kChunk + 16 * q;
         auto load = [&](const int8_t *p, int h) { return load16_masked(p + k + h, clamp16(g.K - k - h)); };
         Operand<E> ob[NT], oa;
