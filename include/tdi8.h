@@ -430,7 +430,9 @@ int swiglu_quant_f8(int type, int T, int N, const void *gate, int ldg, const voi
  * K is at most 131071 (no sum can wrap) and the other sizes at most 2^30; a
  * group_b below one group's extent, a_rows < M without rows, an unknown type
  * or pointers that are not aligned to their element give
- * TDI8_ERR_INVALID_VALUE; C may not overlap an input (TDI8_ERR_ALIASING).
+ * TDI8_ERR_INVALID_VALUE, and so does a product too large for one grid (2^31
+ * threads: from 3 * 10^10 results on, in groups of a row from 2.5 * 10^8 on);
+ * C may not overlap an input (TDI8_ERR_ALIASING).
  * M, N or G = 0 enqueues nothing; K = 0 writes zeros.  16-byte aligned A and B
  * with lda, ldb, group_b and K multiples of 16 take the faster kernels.
  * Ownership, streams and the other errors as for gemm_s8s8s32. */
