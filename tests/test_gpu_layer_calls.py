@@ -184,3 +184,39 @@ def test_other_streams_and_threads():
         th.join()
     for k in range(4):
         same(results[k], want)
+
+
+def test_captured_with_outputs_of_their_own():
+    """A layer's calls captured into a graph, outputs from the graph's memory, replayed over changing inputs."""
+    g = gen(8)
+    x, r, w = normal(g, 24, 512), normal(g, 24, 512), normal(g, 512)
+    B, sb = s8(g, 3, 200, 512), scales(g, 3, 200)
+    off = torch.tensor([0, 5, 5, 24], dtype=torch.int32).cuda()
+
+    def layer():
+        q, scale, h = t.rms_norm(x, w, residual=r)
+        y = t.grouped_gemm(q, scale, B, sb, off)
+        return (q, scale, h, y) + t.swiglu(y[:, :100], y[:, 100:], fmt="f8")
+
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        made = layer()
+    for _ in range(4):
+        x.copy_(normal(g, 24, 512))
+        r.copy_(normal(g, 24, 512))
+        graph.replay()
+        torch.cuda.synchronize()
+        same(made, layer())
+
+
+def test_inference_mode_and_leaves():
+    g = gen(9)
+    x, w = normal(g, 6, 256), normal(g, 256)
+    want = t.rms_norm(x, w)
+    with torch.inference_mode():
+        same(tuple(o.clone() for o in t.rms_norm(x, w)), want)
+    got = t.rms_norm(x.clone().requires_grad_(), torch.nn.Parameter(w.clone()))
+    same(got, want)
+    assert not any(o.requires_grad for o in got)
