@@ -430,8 +430,10 @@ int swiglu_quant_f8(int type, int T, int N, const void *gate, int ldg, const voi
  * K is at most 131071 (no sum can wrap) and the other sizes at most 2^30; a
  * group_b below one group's extent, a_rows < M without rows, an unknown type
  * or pointers that are not aligned to their element give
- * TDI8_ERR_INVALID_VALUE, and so does a product too large for one grid (2^31
- * threads: from 3 * 10^10 results on, in groups of a row from 2.5 * 10^8 on);
+ * TDI8_ERR_INVALID_VALUE, and so does a product whose grid would pass 2^31
+ * threads in every tile that its operands allow: never below 4 * 10^6 tiles of
+ * 64 x 128 results, each group's rows filled up to 64 (scaled_product_plan
+ * says so beforehand).
  * C may not overlap an input (TDI8_ERR_ALIASING).
  * M, N or G = 0 enqueues nothing; K = 0 writes zeros.  16-byte aligned A and B
  * with lda, ldb, group_b and K multiples of 16 take the faster kernels.
@@ -458,6 +460,29 @@ int gemm_s8s8_grouped(int type, int G, int M, int N, int K, const int8_t *A, int
 int gemm_f8f8_block128(int type, int M, int N, int K, const uint8_t *A, int lda, const float *a_scale, int ldas,
                        const uint8_t *B, int ldb, const float *b_scale, int ldbs, void *C, int ldc,
                        hipStream_t stream);
+
+/* Kernel forms of the scaled products, for the plan query below. */
+typedef enum {
+    TDI8_SCALED_NONE = 0,              /* nothing to do */
+    TDI8_SCALED_STREAM = 1,            /* few rows: every wave streams its share of K */
+    TDI8_SCALED_STREAM_UNALIGNED = 2,  /* the same for operands off 16 bytes */
+    TDI8_SCALED_LDS = 3,               /* many rows: both operands staged in LDS */
+    TDI8_SCALED_STAGED = 4             /* many rows off 16 bytes: staged through registers */
+} tdi8_scaled_form;
+
+typedef struct {
+    int form;              /* tdi8_scaled_form */
+    int block_m, block_n;  /* the tile */
+    int threads;           /* of a block */
+    int64_t blocks;        /* of the grid */
+} tdi8_scaled_plan;
+
+/* What gemm_s8s8_grouped (f8 = 0) or gemm_f8f8_block128 (f8 = 1, G = 1) would
+ * enqueue for these sizes on a device of num_cu compute units; aligned: A, B,
+ * lda, ldb, group_b and K are multiples of 16.  TDI8_ERR_INVALID_VALUE where
+ * the call would give it for its sizes.  Needs no device; the calls take the
+ * same decision. */
+int scaled_product_plan(int f8, int type, int G, int M, int N, int K, int aligned, int num_cu, tdi8_scaled_plan *out);
 
 /* Host-side argument check shared by every gemm entry point (no device
  * needed): returns TDI8_OK or the status the entry point would return. */

@@ -473,3 +473,24 @@ def test_streams_captured_together():
         assert torch.equal(y, t.gemm_f8(A, sa, B, sb, dtype=torch.float32))
         assert torch.equal(z, t.grouped_gemm(A8, ra, B8, rb, off, dtype=torch.float32))
         check_f8(y, f8_reference(A.cpu(), sa.cpu(), B.cpu(), sb.cpu()), 2832, torch.float32, f"replay {k}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_more_columns_than_the_smallest_tile_has_a_grid_for(kind):
+    """70 million columns of a row: the products of integers that fp32 holds, rounded once."""
+    g = torch.Generator(device="cuda").manual_seed(50)
+    N, K = 70_000_000, 16
+    note(f"[case] 1 x {N} x {K} {kind}")
+    A = torch.randint(-128, 128, (1, K), device="cuda", generator=g, dtype=torch.int8)
+    B = torch.randint(-128, 128, (N, K), device="cuda", generator=g, dtype=torch.int8)
+    ones = torch.ones(N, device="cuda")
+    want = sum(B[:, k].float() * A[0, k].float() for k in range(K)).to(TYPES[kind])
+    got = t.grouped_gemm(A, ones[:1], B, ones, dtype=TYPES[kind])
+    assert torch.equal(got[0], want)
+    # e4m3: the values 1 .. 8, so that 16 of their products keep within the instruction's 13 bits
+    A8, B8 = ((x & 7).float() + 1 for x in (A, B))
+    want = sum(B8[:, k] * A8[0, k] for k in range(K)).to(TYPES[kind])
+    A8, B8 = A8.to(torch.float8_e4m3fn), B8.to(torch.float8_e4m3fn)
+    blocks = ones[:-(-N // 128)][:, None]
+    got = t.gemm_f8(A8, ones[:1, None], B8, blocks, dtype=TYPES[kind])
+    assert torch.equal(got[0], want)

@@ -183,3 +183,61 @@ def test_native_calls_leave_others_to_python():
         for k in range(len(args)):
             for other in (None, 3, "x", [1], object()):
                 assert call(*args[:k], other, *args[k + 1:], 0, 0) is None
+
+
+# ----- the choice of a product's kernel ------------------------------------------------
+
+def most_tiles(G, M, N):
+    """Tiles of 64 x 128 results, the rows of each group that can have some filled up to 64."""
+    groups = min(G, M)
+    return (M + 63 * groups) // 64 * -(-N // 128)
+
+
+# (f8, groups, M, N, K): few rows and very many columns, the reverse, groups of a row
+HUGE = [(0, 1, 1, 70_000_000, 16), (0, 1, 1, 70_000_000, 1), (0, 1, 8, 68_000_000, 16), (0, 1, 4, 100_000_000, 8),
+        (1, 1, 1, 70_000_000, 16), (1, 1, 8, 68_000_000, 16), (1, 1, 4, 100_000_000, 8), (0, 1, 1, 500_000_000, 1),
+        (0, 1, 250_000_000, 1, 16), (1, 1, 250_000_000, 1, 7), (0, 1, 2 ** 21, 2 ** 13, 64),
+        (0, 4_000_000, 4_000_000, 64, 32), (0, 4_000_000, 4_000_000, 128, 31), (0, 100_000, 200_000, 4096, 64)]
+
+
+@pytest.mark.parametrize("type", [t.F32, t.BF16, t.F16])
+@pytest.mark.parametrize("size", HUGE, ids=lambda s: "x".join(map(str, s)))
+def test_products_of_many_results_have_a_grid(size, type):
+    """A tile whose grid cannot be launched is passed over for one whose grid can."""
+    f8, G, M, N, K = size
+    assert most_tiles(G, M, N) <= 4_000_000
+    for aligned in (K % 16 == 0, False):
+        plan = t.scaled_product_plan(f8, type, G, M, N, K, aligned, 256)
+        assert plan.form != t.SCALED_NONE
+        assert plan.blocks * plan.threads < 2 ** 31
+        tiles = (M + min(G, M) * (plan.block_m - 1)) // plan.block_m * -(-N // plan.block_n)
+        assert plan.blocks == -(-tiles // 8) * 8
+
+
+def test_products_without_a_grid_are_refused():
+    for size in (0, 1, 2 ** 30, 2 ** 12, 64), (0, 1, 2 ** 30, 2 ** 30, 64), (0, 2 ** 26, 2 ** 26, 1024, 64):
+        for aligned in (0, 1):
+            f8, G, M, N, K = size
+            assert most_tiles(G, M, N) > 4_000_000
+            with pytest.raises(t.TDI8Error) as e:
+                t.scaled_product_plan(f8, t.BF16, G, M, N, K, aligned, 256)
+            assert e.value.status == t.ERR_INVALID_VALUE
+
+
+def test_plan_of_ordinary_sizes():
+    """The tiles of sizes whose measurements the code names."""
+    for size, want in (((1, 1, 16, 4096, 4096, 1), (t.SCALED_STREAM, 16, 16)),
+                       ((1, 1, 4096, 4096, 4096, 1), (t.SCALED_LDS, 256, 256)),
+                       ((1, 1, 1000, 3000, 777, 0), (t.SCALED_STAGED, 64, 128)),
+                       ((0, 8, 1000, 1501, 777, 0), (t.SCALED_STAGED, 64, 128)),
+                       ((0, 64, 64, 4096, 2048, 1), (t.SCALED_STREAM, 16, 32)),
+                       ((0, 16, 16384, 4096, 4096, 1), (t.SCALED_LDS, 256, 256))):
+        f8, G, M, N, K, aligned = size
+        plan = t.scaled_product_plan(f8, t.BF16, G, M, N, K, aligned, 256)
+        assert (plan.form, plan.block_m, plan.block_n) == want, size
+    for empty in (0, 0, 5, 5), (0, 3, 0, 5), (1, 1, 5, 0):
+        assert t.scaled_product_plan(*empty[:1], t.F32, *empty[1:], 64, 1, 256).form == t.SCALED_NONE
+    for bad in (0, 3, 1, 1, 1, 1, 1, 256), (1, 0, 2, 1, 1, 1, 1, 256), (0, 0, 1, 1, 1, 131072, 1, 256), \
+            (0, 0, 1, -1, 1, 1, 1, 256), (0, 0, 1, 1, 1, 1, 1, 0):
+        with pytest.raises(t.TDI8Error):
+            t.scaled_product_plan(*bad)

@@ -71,6 +71,14 @@ class Plan(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+SCALED_NONE, SCALED_STREAM, SCALED_STREAM_UNALIGNED, SCALED_LDS, SCALED_STAGED = range(5)
+
+
+class ScaledPlan(ctypes.Structure):
+    _fields_ = [("form", ctypes.c_int), ("block_m", ctypes.c_int), ("block_n", ctypes.c_int),
+                ("threads", ctypes.c_int), ("blocks", ctypes.c_int64)]
+
+
 _i, _p, _f = ctypes.c_int, ctypes.c_void_p, ctypes.c_float
 _GEMM_ARGS = [_i, _i, _i, _p, _i, _p, _i, _p, _i, _p]
 _SIGNATURES = {
@@ -97,6 +105,7 @@ _SIGNATURES = {
     "swiglu_quant_f8": (_i, [_i] * 3 + [_p, _i, _p, _i, _p, _i, _p, _i, _p]),
     "gemm_s8s8_grouped": (_i, [_i] * 5 + [_p, _i, _i, _p, _p, _p, _p, _i, ctypes.c_int64, _p, _p, _i, _p]),
     "gemm_f8f8_block128": (_i, [_i] * 4 + [_p, _i, _p, _i, _p, _i, _p, _i, _p, _i, _p]),
+    "scaled_product_plan": (_i, [_i] * 8 + [ctypes.POINTER(ScaledPlan)]),
     "tdi8_status_string": (ctypes.c_char_p, [_i]),
     "tdi8_last_hip_error": (_i, []),
     "tdi8_kernel_code_hash": (ctypes.c_char_p, []),
@@ -562,6 +571,16 @@ def gemm_s8s8_grouped(type, G, M, N, K, A, lda, a_rows, a_scale, rows, offsets, 
 def gemm_f8f8_block128(type, M, N, K, A, lda, a_scale, ldas, B, ldb, b_scale, ldbs, C, ldc, stream=0) -> int:
     _int32(type=type, M=M, N=N, K=K, lda=lda, ldas=ldas, ldb=ldb, ldbs=ldbs, ldc=ldc)
     return _lib.gemm_f8f8_block128(type, M, N, K, A, lda, a_scale, ldas, B, ldb, b_scale, ldbs, C, ldc, stream)
+
+
+def scaled_product_plan(f8, type, G, M, N, K, aligned, num_cu) -> ScaledPlan:
+    """What the scaled product of these sizes would enqueue; raises TDI8Error for sizes it refuses."""
+    _int32(type=type, G=G, M=M, N=N, K=K, num_cu=num_cu)
+    out = ScaledPlan()
+    st = _lib.scaled_product_plan(1 if f8 else 0, type, G, M, N, K, 1 if aligned else 0, num_cu, ctypes.byref(out))
+    if st != OK:
+        raise TDI8Error(st)
+    return out
 
 
 def _product_out(M, N, dtype, like, out, stream):

@@ -164,10 +164,11 @@ def build(jobs: int | None = None, verbose: bool = False, extra_flags: list[str]
                   "-o", os.path.join(bdir, "abi.o")])
     units.append([HIPCC, *flags, "-x", "hip", "-c", os.path.join(CSRC, "selector.cpp"),
                   "-o", os.path.join(bdir, "selector.o")])
-    # the 8-bit layer operators: entry points, the row kernels by type, the
-    # scaled products by operand type
-    units.append([HIPCC, *flags, "-x", "hip", "-c", os.path.join(CSRC, "layer_ops.cpp"),
-                  "-o", os.path.join(bdir, "layer_ops.o")])
+    # the 8-bit layer operators: entry points and the choice of a product's
+    # kernel, the row kernels by type, the scaled products by operand type
+    for name in ("layer_ops", "product_choice"):
+        units.append([HIPCC, *flags, "-x", "hip", "-c", os.path.join(CSRC, name + ".cpp"),
+                      "-o", os.path.join(bdir, name + ".o")])
     for ty in ("F32", "Bf16", "F16"):
         units.append([HIPCC, *flags, f"-DTDI8_ROWS_TYPE={ty}", f"-DTDI8_ROWS_REGISTER=register_rows_{ty.lower()}",
                       "-c", os.path.join(CSRC, "quant_rows.hip"), "-o", os.path.join(bdir, f"quant_rows_{ty}.o")])

@@ -35,9 +35,6 @@ const RowKernels *row_kernels(int type) {
     return &table[type];
 }
 
-// Sizes stay this far from the end of int, so that a kernel may round one up
-// to its tile.
-constexpr int kMostColumns = 1 << 30;
 constexpr int kBlock = 128;
 
 // Checks of a row operator; lds is the leading dimension of the scales (1 for s8).
@@ -155,7 +152,6 @@ int act_entry(int fmt, int type, int T, int N, const void *gate, int ldg, const 
     return rows_entry(kOpAct, fmt, type, g, stream);
 }
 
-// e4m3 products with fp32 results have kernels of their own (F8Wide).
 const ProductKernels *product_kernels(bool f8, int type) {
     static const ProductKernels *table = [] {
         static ProductKernels k[3];
@@ -167,14 +163,13 @@ const ProductKernels *product_kernels(bool f8, int type) {
     return &table[!f8 ? 0 : type == TDI8_F32 ? 2 : 1];
 }
 
-// LDS tile kernels of an operand type, and their tiles.
-struct TileSet {
+// LDS tile kernels of an operand type, in the order of lds_tiles.
+struct TileKernels {
     const void *kernel[kLdsTiles];
-    const Tile *tile;
 };
-const TileSet &tile_set(bool f8, int type) {
-    static const TileSet *table = [] {
-        static TileSet t[3] = {{{}, kGroupedTile}, {{}, kF8Tile}, {{}, kF8WideTile}};
+const TileKernels &tile_kernels(bool f8, int type) {
+    static const TileKernels *table = [] {
+        static TileKernels t[3];
         register_grouped_tiles(t[0].kernel);
         register_f8_tiles(t[1].kernel);
         register_f8wide_tiles(t[2].kernel);
@@ -193,8 +188,7 @@ int check_product(bool f8, const ProductArgs &g) {
     const int64_t kmin = g.K > 1 ? g.K : 1;
     if (g.lda < kmin || g.ldb < kmin || g.ldc < (g.N > 1 ? g.N : 1)) return TDI8_ERR_INVALID_VALUE;
     if (f8 && (g.ldas < (kb > 1 ? kb : 1) || g.ldbs < (kb > 1 ? kb : 1))) return TDI8_ERR_INVALID_VALUE;
-    // an int32 sum of K products of int8 cannot wrap
-    if (!f8 && g.K > 131071) return TDI8_ERR_INVALID_VALUE;
+    if (!f8 && g.K > kMostK8) return TDI8_ERR_INVALID_VALUE;
     if (!g.offsets && g.G > 1) return TDI8_ERR_NULL_POINTER;
     if (!g.rows && g.a_rows < g.M) return TDI8_ERR_INVALID_VALUE;
     if (g.M == 0 || g.N == 0 || g.G == 0) return TDI8_OK;
@@ -230,66 +224,20 @@ int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
     if (st != TDI8_OK) return st;
     const bool al = aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 16 == 0 && g.ldb % 16 == 0 && g.K % 16 == 0 &&
                     (g.G == 1 || g.group_b % 16 == 0);
-    // The choice goes by the sizes alone: how the rows fall to the groups is
-    // known to the device only.
-    const int64_t groups = g.G < g.M ? g.G : g.M;  // that can have rows
-    const int64_t rows = (g.M + groups - 1) / groups;
-    // row tiles of height bm: half a tile of each group is lost on average
-    auto expected = [&](int bm, int bn) {
-        const int64_t m = groups == 1 ? (g.M + bm - 1) / bm : std::max<int64_t>(groups, g.M / bm + groups / 2);
-        return m * ((g.N + bn - 1) / bn);
-    };
     const bool near = !f8 || (256 * std::max(g.lda, g.ldb) + g.K < INT_MAX && 4 * (256 * g.ldas + g.K) < INT_MAX);
+    ProductChoice c{};
+    if (!choose_product(f8, g.type, g.G, g.M, g.N, g.K, al, near, units, &c)) return TDI8_ERR_INVALID_VALUE;
+    g.tiles_m = c.tiles_m;
+    g.tiles_n = c.tiles_n;
     const ProductKernels &pk = *product_kernels(f8, g.type);
-    const void *kernel = nullptr;
-    int bm = 0, bn = 0, threads = 0;
-    auto take = [&](const void *k, const Tile &t) {
-        kernel = k;
-        bm = t.bm;
-        bn = t.bn;
-        threads = t.threads;
-    };
-    const int64_t lds = expected(64, 128);
-    if (groups > 1 && (rows <= 2 || (rows <= 32 && lds < units))) {
-        // Groups of few rows: most row tiles hold few, so that B is read once
-        // (int8: 256 groups of 2 rows on average, 1024 x 2048: 86 us, by LDS
-        // tiles 118; 64 of 2, 2048 x 4096: 85 and 78; 8 of 16, 1024 x 4096: 10.4
-        // and 18.8; 8 of 8, 4096 x 4096, where many have two row tiles: 33 and 27.6).
-        take(al ? pk.stream[kGroupStream] : pk.unaligned_group, kStreamTile[kGroupStream]);
-    } else {
-        // the least of the tiles' measured costs; equal ones to the first
-        float best = 0.0f;
-        auto weigh = [&](const void *k, const Tile &t) {
-            const int64_t round = static_cast<int64_t>(units) * t.per_cu;
-            const int64_t rounds = (expected(t.bm, t.bn) + round - 1) / round;
-            const float cost = t.start + rounds * (t.fixed + t.per_4096 * g.K / 4096.0f);
-            if (kernel && cost >= best) return;
-            best = cost;
-            take(k, t);
-        };
-        // Streams while the LDS tiles leave compute units idle (512 x 4096 x
-        // 4096 e4m3, 256 of those: 25 us against 22) or where B is all there is
-        // to read (8 x 32768 x 4096: 25 against 28.6); no tile of twice the rows.
-        const Tile *streams = al ? kStreamTile : kUnalignedTile;
-        if (lds < units || rows <= 8)
-            for (int i = 0; i < (al ? +kGroupStream : +kUnalignedStreams); ++i)
-                if (streams[i].bm < 2 * rows || i == 0) weigh(al ? pk.stream[i] : pk.unaligned[i], streams[i]);
-        if (al && near) {
-            const TileSet &set = tile_set(f8, g.type);
-            for (int i = 0; i < kLdsTiles && set.kernel[i]; ++i) weigh(set.kernel[i], set.tile[i]);
-        } else {
-            for (const Tile &t : kStagedTile) weigh(pk.staged, t);
-        }
-    }
-    // every group that has rows ends in at most one partial tile
-    const int64_t tm = (g.M + groups * (bm - 1)) / bm;
-    const int64_t tn = (static_cast<int64_t>(g.N) + bn - 1) / bn;
-    if (tm > INT_MAX || tm * tn > INT_MAX / threads - 8) return TDI8_ERR_INVALID_VALUE;
-    g.tiles_m = static_cast<int>(tm);
-    g.tiles_n = static_cast<int>(tn);
-    const unsigned blocks = static_cast<unsigned>((tm * tn + 7) / 8 * 8);
+    const void *kernel = c.form == TDI8_SCALED_STREAM             ? pk.stream[c.index]
+                         : c.form == TDI8_SCALED_STREAM_UNALIGNED ? (c.index == kGroupStream ? pk.unaligned_group
+                                                                                             : pk.unaligned[c.index])
+                         : c.form == TDI8_SCALED_LDS              ? tile_kernels(f8, g.type).kernel[c.index]
+                                                                  : pk.staged;
     void *args[] = {&g};
-    const hipError_t e = hipLaunchKernel(kernel, dim3(blocks), dim3(static_cast<unsigned>(threads)), args, 0, stream);
+    const hipError_t e = hipLaunchKernel(kernel, dim3(static_cast<unsigned>(c.blocks)),
+                                         dim3(static_cast<unsigned>(c.threads)), args, 0, stream);
     return e == hipSuccess ? TDI8_OK : hip_fail(e);
 }
 

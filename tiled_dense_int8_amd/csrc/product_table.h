@@ -1,6 +1,8 @@
-// Kernels of the scaled products, by operand type and tile.
+// Kernels of the scaled products, by operand type and tile, and the choice
+// between them.
 #pragma once
 
+#include "../../include/tdi8.h"
 #include "scaled_product.h"
 
 namespace tdi8 {
@@ -48,6 +50,31 @@ constexpr Tile kUnalignedTile[kUnalignedStreams] = {{8, 16, 512, 1, 3.0f, 0.2f, 
                                                     {32, 32, 512, 1, 2.7f, 1.4f, 7.6f},
                                                     {32, 64, 512, 1, 0.0f, 4.5f, 11.0f}};
 constexpr Tile kStagedTile[kStagedTiles] = {{64, 128, 512, 1, 0.0f, 2.2f, 46.0f}, {64, 128, 512, 2, 0.0f, 3.2f, 54.0f}};
+
+// The LDS tiles of an operand type (those with threads).  e4m3 products with
+// fp32 results have kernels of their own (F8Wide).
+inline const Tile *lds_tiles(bool f8, int type) {
+    return !f8 ? kGroupedTile : type == TDI8_F32 ? kF8WideTile : kF8Tile;
+}
+
+// Sizes stay this far from the end of int, so that a kernel may round one up
+// to its tile; a sum of kMostK8 products of int8 cannot wrap an int32.
+constexpr int kMostColumns = 1 << 30;
+constexpr int kMostK8 = 131071;
+
+// How a scaled product runs: a form (tdi8_scaled_form) and its entry in that
+// form's table, the tile, the row tiles (a bound, whatever the groups' sizes),
+// the column tiles and the blocks of the grid.
+struct ProductChoice {
+    int form, index;
+    int bm, bn, threads;
+    int tiles_m, tiles_n;
+    int64_t blocks;
+};
+// al: operands on 16 bytes; near: they fit the buffer addresses of the LDS
+// tiles.  M, N, G > 0.  False if no tile's grid can be launched (2^31 threads).
+bool choose_product(bool f8, int type, int64_t G, int64_t M, int64_t N, int64_t K, bool al, bool near, int units,
+                    ProductChoice *out);
 
 struct ProductKernels {
     const void *stream[kStreamTiles];
