@@ -4,7 +4,8 @@ import torch
 
 import tiled_dense_int8_amd as t
 from helpers import note
-from layer_helpers import TYPES, act_values, check_quantised, norm_steps, norm_sum, norm_values, quantise, strided
+from layer_helpers import (TYPES, act_values, check_quantised, e4m3_nearest, norm_steps, norm_sum, norm_values, quantise,
+                           strided)
 
 pytestmark = pytest.mark.gpu
 
@@ -275,3 +276,50 @@ def test_f8_quotients_next_to_a_border_go_by_their_fp32_form():
         x[0, 1 + k], weight[1 + k], want[1 + k] = h, w, q
     q, _ = t.rms_norm(x.cuda(), weight.cuda(), fmt="f8")
     assert torch.equal(q.float().cpu()[0], want)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_act_f8_values_far_out(kind):
+    """The e4m3 form of gates whose exponential overflows, of large ones and of zeros of both signs."""
+    g = torch.tensor([-1e4, -200, -104, -100, -89, -88, -87.5, -81, -80, -79, -40, -20, -1, -0.0, 0.0, 1, 20, 80, 100,
+                      1e4])
+    gate = g.repeat(4, 30)[:, :577].to(TYPES[kind])
+    up = torch.stack([torch.ones(577), torch.full((577,), 1e3), torch.full((577,), -3e-3),
+                      torch.randn(577, generator=gen(4))]).to(TYPES[kind])
+    for a in (gate, gate.clamp(max=-85)):
+        note(f"[act] f8 far out {kind}")
+        q, scale = t.swiglu(a.cuda(), up.cuda(), fmt="f8")
+        v, inv = act_values(a, up)
+        want, s = quantise(v, inv, "f8")
+        assert torch.equal(q.cpu().float().double(), e4m3_nearest(want))
+        # the largest value may be a 32-bit one, off by 10 steps of 2^-24, before
+        # the scale's rounding; scales below fp32's normal range round to a
+        # multiple of 2^-149
+        assert ((scale.cpu().double() - s).abs() <= s * 11 * 2.0 ** -24 + 2.0 ** -150).all()
+
+
+# (gate, up) beside values of 2^-60: gates below -80 whose value is nothing all
+# the same, and gates so small that their half is no normal fp32 number
+BESIDE = [(-128.0, 2.0 ** 33), (-96.0, 2.0 ** 33), (-100.0, 2.0 ** 39), (-90.0, 2.0 ** 34), (-81.0, 2.0 ** 32),
+          (-80.5, 2.0 ** 25), (-4096.0, 2.0 ** 20), (-80.0, -2.0 ** 33), (3 * 2.0 ** -149, 2.0 ** 89),
+          (5 * 2.0 ** -149, -2.0 ** 88), (7 * 2.0 ** -149, 2.0 ** 39), (2.0 ** -133, 2.0 ** 72),
+          (3 * 2.0 ** -130, 2.0 ** 60), (2.0 ** 100, 2.0 ** -160 * 3), (2.0 ** 90, 2.0 ** -149)]
+
+
+@pytest.mark.parametrize("fmt", ["s8", "f8"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_act_far_values_beside_small_ones(kind, fmt):
+    """Values whose gate or other half is far out, where the largest of the row (block) is about 2^-60."""
+    for N in (5, 300, 7000, 40000):
+        # among others in a vector of eight, and vectors of nothing else
+        for far in (torch.arange(N) % 97 == 3, torch.arange(N) // 8 % 12 == 1):
+            gate = torch.ones(len(BESIDE), N)
+            up = torch.rand(len(BESIDE), N, generator=gen(11)) * 2.0 ** -60 + 2.0 ** -60
+            for row, (a, b) in enumerate(BESIDE):
+                gate[row, far], up[row, far] = a, b
+            gate, up = gate.to(TYPES[kind]), up.to(TYPES[kind])
+            what = f"{kind} {fmt} N={N}"
+            note(f"[act] beside {what}")
+            q, scale = t.swiglu(gate.cuda(), up.cuda(), fmt=fmt)
+            v, inv = act_values(gate, up)
+            check_quantised(q, scale, v, inv, fmt, what)

@@ -43,7 +43,7 @@ namespace tdi8 {
 
 // Eight elements as 32-bit words: one each for F32, two elements in each for
 // the 16-bit types.
-// kHalf: products of two magnitudes stay below 2^40.
+// kHalf: products of two magnitudes stay below 2^32, and halves are normal fp32 numbers.
 struct F32 {
     static constexpr bool kHalf = false;
     static constexpr int kBytes = 4;
@@ -200,9 +200,12 @@ __device__ __forceinline__ double value64(float a, float b) {
 // above: e^-g = 2^hi (1 + lo ln 2) with hi + lo = -g log2 e to twice the
 // precision (2^hi and the reciprocal are off by 2^-23 each, the other six
 // operations by 2^-24).  Below g = -80 it takes e^80, so that the exponential
-// cannot overflow; the value is then below 2 * 10^-35 |g u|, nothing next to
-// 2^-60 while |g u| is at most 2^40 (values32 sees to that).  NaN and
-// infinities come out as NaN or an infinity.
+// cannot overflow; the value is then below 2 * 10^-35 |g u| instead of next to
+// nothing.  While |g u| is at most 2^32 that is 10^-7 of a row's 2^-60 and 4 *
+// 10^-5 of the f8 quotient's scale, against a border to the least e4m3 value
+// at 2^-10.  A gate so small that half of it is no normal number is off by
+// 2^-150; times |u| up to 2^40 that is 2^-50 of 2^-60.  values32 sees to both
+// limits.  NaN and infinities come out as NaN or an infinity.
 template <int OP>
 __device__ __forceinline__ float value32(float a, float b) {
     if constexpr (OP == kOpNorm) {
@@ -219,10 +222,11 @@ __device__ __forceinline__ float value32(float a, float b) {
     }
 }
 // Eight of them; one is an infinity where the fp32 form may not hold, which
-// sends the row (block) to the fp64 path.
+// sends the row (block) to the fp64 path: where the largest |g| times the
+// largest |u| of the eight passes 2^32, or the latter 2^40 (2^-8 times it 2^32).
 template <class T, int OP>
 __device__ __forceinline__ void values32(const Vec8<T> &a, const Vec8<T> &b, float *v) {
-    float am = 0.0f, bm = 0.0f;
+    float am = 0x1p-8f, bm = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float x = a.get(i), y = b.get(i);
@@ -230,7 +234,7 @@ __device__ __forceinline__ void values32(const Vec8<T> &a, const Vec8<T> &b, flo
         am = fmaxf(am, fabsf(x));
         bm = fmaxf(bm, fabsf(y));
     }
-    if constexpr (OP == kOpAct && !T::kHalf) v[0] = am * bm > 0x1p40f ? __builtin_inff() : v[0];
+    if constexpr (OP == kOpAct && !T::kHalf) v[0] = am * bm > 0x1p32f ? __builtin_inff() : v[0];
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
