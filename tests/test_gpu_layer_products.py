@@ -494,3 +494,52 @@ def test_more_columns_than_the_smallest_tile_has_a_grid_for(kind):
     blocks = ones[:-(-N // 128)][:, None]
     got = t.gemm_f8(A8, ones[:1, None], B8, blocks, dtype=TYPES[kind])
     assert torch.equal(got[0], want)
+
+
+LOUD_CASES = STREAM_CASES + [(M, N, K) for M, N, K in LARGE if M * N < 10 ** 7] + \
+    [(700, 640, 1408), (2100, 4096, 256), (1000, 1501, 1101)]
+
+
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+@pytest.mark.parametrize("size", LOUD_CASES, ids=lambda s: "x".join(map(str, s)))
+def test_f8_large_products_that_cancel(size, kind):
+    """Two products of +-448^2 among each 16, the others 1: with sums in 32
+    bits every partial sum is a whole number below 2^24, so the result is the
+    exact one, rounded once to the type."""
+    M, N, K = size
+    note(f"[case] cancelling {size} {kind}")
+    a, b = torch.ones(M, K), torch.ones(N, K)
+    g = gen(sum(size))
+    a[:, 0::16], b[:, 0::16] = 448, 448
+    a[:, 5::16], b[:, 5::16] = -448, 448
+    if K % 16 in range(1, 6):  # a last piece that holds the first of the two only
+        a[:, K - K % 16] = 1
+        b[:, K - K % 16] = 1
+    some = torch.arange(K) % 16 == 9  # and values that differ from row to row
+    a[:, some] = torch.randint(-8, 9, (M, int(some.sum())), generator=g).float()
+    want = a.double().mm(b.double().t())
+    kb, nb = -(-K // 128), -(-N // 128)
+    f8 = torch.float8_e4m3fn
+    got = t.gemm_f8(a.to(f8).cuda(), torch.ones(M, kb).cuda(), b.to(f8).cuda(), torch.ones(nb, kb).cuda(),
+                    dtype=TYPES[kind])
+    assert torch.equal(got.cpu(), want.to(TYPES[kind]))
+
+
+@pytest.mark.parametrize("size", [(16, 300, 2832), (100, 999, 1101), (513, 640, 2048)], ids=lambda s: "x".join(map(str, s)))
+def test_f8_bf16_sums_of_loud_channels(size):
+    """bf16 results within the documented bound of the instruction's sums, loud channels or not."""
+    M, N, K = size
+    for loud in (1, 30):
+        g = gen(sum(size))
+        A, B = torch.randn(M, K, generator=g) * 8, e4m3(g, N, K)
+        A[:, 7::128] *= loud
+        A = A.clamp(-448, 448).to(torch.float8_e4m3fn)
+        sa, sb = scales(g, M, -(-K // 128)), scales(g, -(-N // 128), -(-K // 128))
+        got = t.gemm_f8(A.cuda(), sa.cuda(), B.cuda(), sb.cuda())
+        want, size_of, pieces = f8_reference(A, sa, B, sb)
+        # 15 of 16 products of a piece, each by less than 2^-13 of the piece's
+        # largest, whose bound `pieces` counts 16 times; sums in 32 bits and
+        # the type's rounding as check_f8 has them (127 * 2^-23 + 40 * 2^-24 < 2^-15)
+        off = (got.cpu().double() - want).abs()
+        absolute = pieces * (15 / 16) * 2.0 ** -13 + size_of * 2.0 ** -15
+        assert (off <= absolute * (1 + 2.0 ** -8) + want.abs() * 2.0 ** -8).all()

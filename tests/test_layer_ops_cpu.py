@@ -241,3 +241,10 @@ def test_plan_of_ordinary_sizes():
             (0, 0, 1, -1, 1, 1, 1, 256), (0, 0, 1, 1, 1, 1, 1, 0):
         with pytest.raises(t.TDI8Error):
             t.scaled_product_plan(*bad)
+
+
+def test_only_bf16_results_of_e4m3_take_the_256_wide_tile():
+    """Results of fp16 and fp32 need sums in 32 bits, whose kernels have other tiles."""
+    for type, want in ((t.BF16, (256, 256)), (t.F16, (128, 128)), (t.F32, (128, 128))):
+        plan = t.scaled_product_plan(1, type, 1, 4096, 4096, 4096, 1, 256)
+        assert plan.form == t.SCALED_LDS and (plan.block_m, plan.block_n) == want

@@ -5,7 +5,7 @@
 // tile's part of a whole scale block; since the block scales are no powers of
 // two it starts from zero, and acc += part * (a_scale * b_scale) in fp32
 // follows: 4 multiply-adds a lane for 32 cycles of the matrix core, which run
-// beside it (fp32 results take F8Wide's four bf16 instructions instead).  A
+// beside it (fp32 and fp16 results take F8Wide's four bf16 instructions instead).  A
 // lane's part belongs to one row of A (B is the instruction's first operand)
 // and a wave's columns to one block of 128, so the scale is one register per
 // 16 rows.

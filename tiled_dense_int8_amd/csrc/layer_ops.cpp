@@ -155,12 +155,12 @@ int act_entry(int fmt, int type, int T, int N, const void *gate, int ldg, const 
 const ProductKernels *product_kernels(bool f8, int type) {
     static const ProductKernels *table = [] {
         static ProductKernels k[3];
-        register_products_s8(&k[0]);
-        register_products_f8(&k[1]);
-        register_products_f8wide(&k[2]);
+        register_products_s8(&k[kProductS8]);
+        register_products_f8(&k[kProductF8]);
+        register_products_f8wide(&k[kProductF8Wide]);
         return k;
     }();
-    return &table[!f8 ? 0 : type == TDI8_F32 ? 2 : 1];
+    return &table[product_type(f8, type)];
 }
 
 // LDS tile kernels of an operand type, in the order of lds_tiles.
@@ -170,12 +170,12 @@ struct TileKernels {
 const TileKernels &tile_kernels(bool f8, int type) {
     static const TileKernels *table = [] {
         static TileKernels t[3];
-        register_grouped_tiles(t[0].kernel);
-        register_f8_tiles(t[1].kernel);
-        register_f8wide_tiles(t[2].kernel);
+        register_grouped_tiles(t[kProductS8].kernel);
+        register_f8_tiles(t[kProductF8].kernel);
+        register_f8wide_tiles(t[kProductF8Wide].kernel);
         return t;
     }();
-    return table[!f8 ? 0 : type == TDI8_F32 ? 2 : 1];
+    return table[product_type(f8, type)];
 }
 
 // Checks of a scaled product; kb: scales of a row of A (1, or K's blocks of 128).

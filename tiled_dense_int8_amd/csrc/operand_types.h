@@ -52,7 +52,7 @@ struct F8 {
     using Acc = f32x4;
     static constexpr bool kBlockScales = true;
 };
-struct F8Wide {  // e4m3 with fp32 results
+struct F8Wide {  // e4m3 with fp32 and fp16 results
     using Acc = f32x4;
     static constexpr bool kBlockScales = true;
 };
@@ -77,11 +77,18 @@ struct Operand<S8> {
 
 // e4m3: one v_mfma_f32_16x16x128_f8f6f4, whose 128 products of K are exactly a
 // scale block, then acc += scale * part in fp32.
-// The instruction adds the 16 products of a 16-byte piece after cutting each to
-// a multiple of 2^-13 of the largest one's power of two (measured: 2^5 + 2^-8
-// is exact within a piece, 2^6 + 2^-8 gives 2^6; between pieces sums are fp32).
-// On normal operands a result is off by 1.5 * 10^-5 of the results' size, far
-// below half a step of the 16-bit types (2^-9, 2^-12).
+// The instruction adds the 16 products of a 16-byte piece after cutting each,
+// toward zero, to a multiple of 2^-13 of the largest one's power of two
+// (measured: 2^5 + 2^-8 is exact within a piece, 2^6 + 2^-8 gives 2^6; between
+// pieces sums are fp32).  So a result is off by at most 15 * 2^-13 times the
+// sum of the pieces' largest magnitudes.  On normal operands that comes to
+// 2.7 * 10^-5 of the results' root mean square, with a channel 30 times louder
+// in each block to 1.3 * 10^-4 (6 * 10^-4 at worst); where all products have
+// one sign and one of each 16 is far the largest, a result loses up to 4.8 *
+// 10^-4 of itself, and never 2^-9, half a step of bf16; where large products
+// cancel, what is left can be lost.  For bf16 results the full rate is taken
+// for that: an e4m3 operand itself is rounded by up to 2^-4 of a value, the
+// products that are cut among them.  Half a step of fp16 (2^-12) it can reach.
 template <>
 struct Operand<F8> {
     i32x8 v;
@@ -99,7 +106,7 @@ struct Operand<F8> {
     }
 };
 
-// For fp32 results: e4m3 widened to bf16 (exact), whose products are added in
+// For fp32 and fp16 results: e4m3 widened to bf16 (exact), whose products are added in
 // fp32: v_mfma_f32_16x16x32_bf16, four a chunk, at half the rate.
 template <>
 struct Operand<F8Wide> {

@@ -51,10 +51,18 @@ constexpr Tile kUnalignedTile[kUnalignedStreams] = {{8, 16, 512, 1, 3.0f, 0.2f, 
                                                     {32, 64, 512, 1, 0.0f, 4.5f, 11.0f}};
 constexpr Tile kStagedTile[kStagedTiles] = {{64, 128, 512, 1, 0.0f, 2.2f, 46.0f}, {64, 128, 512, 2, 0.0f, 3.2f, 54.0f}};
 
-// The LDS tiles of an operand type (those with threads).  e4m3 products with
-// fp32 results have kernels of their own (F8Wide).
+// Operand types of the kernels.  e4m3 products take the matrix instruction's
+// own sums for bf16 results only: they can be off by half a step of fp16
+// (operand_types.h).  With fp16 and fp32 results e4m3 is widened (on one card
+// 4096^3 144 us to fp16, 89 to bf16; 16 x 4096 x 4096 5.4 and 5.2).
+enum { kProductS8 = 0, kProductF8 = 1, kProductF8Wide = 2 };
+inline int product_type(bool f8, int type) {
+    return !f8 ? kProductS8 : type == TDI8_BF16 ? kProductF8 : kProductF8Wide;
+}
+// The LDS tiles of an operand type (those with threads).
 inline const Tile *lds_tiles(bool f8, int type) {
-    return !f8 ? kGroupedTile : type == TDI8_F32 ? kF8WideTile : kF8Tile;
+    const Tile *tiles[] = {kGroupedTile, kF8Tile, kF8WideTile};
+    return tiles[product_type(f8, type)];
 }
 
 // Sizes stay this far from the end of int, so that a kernel may round one up
