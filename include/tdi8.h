@@ -504,14 +504,19 @@ const char *tdi8_status_string(int status);
  * thread for the caller after an entry point returned TDI8_ERR_HIP. */
 int tdi8_last_hip_error(void);
 
-/* Identity of the GPU code compiled into this library: the first 16 hex
- * digits of the SHA-256 of the gfx950 code objects of every configuration,
- * in configuration order (static string; the caller must not free it).  Two
- * builds report the same value exactly when their kernels are the same
- * machine code, so a measurement taken on one build (a counter pass, a
- * kernel trace) can record it and be matched against the library that runs
- * later.  Not part of the pages' method: a build identity for measurements. */
+/* Identity of the GPU code of the GEMM and convolution kernels compiled into
+ * this library: the first 16 hex digits of the SHA-256 of the gfx950 code
+ * objects of every configuration, in configuration order (static string; the
+ * caller must not free it).  Two builds report the same value exactly when
+ * those kernels are the same machine code, so a measurement taken on one build
+ * (a counter pass, a kernel trace) can record it and be matched against the
+ * library that runs later.  Not part of the pages' method: a build identity
+ * for measurements. */
 const char *tdi8_kernel_code_hash(void);
+
+/* The same for the kernels of the 8-bit layer operators (rows, grouped and
+ * block-scaled products). */
+const char *tdi8_layer_code_hash(void);
 
 #ifdef __cplusplus
 }

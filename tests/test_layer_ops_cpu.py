@@ -248,3 +248,27 @@ def test_only_bf16_results_of_e4m3_take_the_256_wide_tile():
     for type, want in ((t.BF16, (256, 256)), (t.F16, (128, 128)), (t.F32, (128, 128))):
         plan = t.scaled_product_plan(1, type, 1, 4096, 4096, 4096, 1, 256)
         assert plan.form == t.SCALED_LDS and (plan.block_m, plan.block_n) == want
+
+
+def test_layer_code_hash_covers_every_layer_kernel():
+    """The hash is that of all objects that hold layer kernels; with the configurations' it covers the library's."""
+    import glob
+    import hashlib
+    import os
+    import re
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "tiled_dense_int8_amd"))
+    import build as b
+    h = t.tdi8_layer_code_hash()
+    assert len(h) == 16 and int(h, 16) >= 0 and h != t.tdi8_kernel_code_hash()
+    cos = [os.path.join(b.BUILD, name + ".o.co") for name in b.LAYER_OBJECTS]
+    if all(os.path.exists(c) for c in cos):
+        d = hashlib.sha256()
+        for c in cos:
+            d.update(open(c, "rb").read())
+        assert d.hexdigest()[:16] == h
+    # no source with a kernel's definition is built into an object of neither list
+    sources = {os.path.splitext(os.path.basename(p))[0] for p in glob.glob(os.path.join(b.CSRC, "*.hip"))}
+    listed = {re.sub("_(S8|F8|F8Wide|F32|Bf16|F16)$", "", name) for name in b.LAYER_OBJECTS}
+    assert {s.replace("stream_product", "stream") for s in sources} == listed | {"instantiate", "ceilings"}

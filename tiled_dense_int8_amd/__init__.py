@@ -109,6 +109,7 @@ _SIGNATURES = {
     "tdi8_status_string": (ctypes.c_char_p, [_i]),
     "tdi8_last_hip_error": (_i, []),
     "tdi8_kernel_code_hash": (ctypes.c_char_p, []),
+    "tdi8_layer_code_hash": (ctypes.c_char_p, []),
 }
 for _name, (_res, _args) in _SIGNATURES.items():
     _fn = getattr(_lib, _name)
@@ -233,6 +234,10 @@ def tdi8_last_hip_error() -> int:
 
 def tdi8_kernel_code_hash() -> str:
     return _lib.tdi8_kernel_code_hash().decode()
+
+
+def tdi8_layer_code_hash() -> str:
+    return _lib.tdi8_layer_code_hash().decode()
 
 
 # ----- torch convenience -----------------------------------------------------------

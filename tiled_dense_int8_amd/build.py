@@ -9,7 +9,8 @@ configuration's column-major kernel (the one the selection's occupancy is
 taken on) is read from the AMDGPU metadata note of the gfx950 code object
 this build just produced, and compiled into the library as a table
 (_build/kernel_resources.cpp): tile_config_info reports it.  The same file
-carries the SHA-256 of those code objects (tdi8_kernel_code_hash).
+carries the SHA-256 of those code objects (tdi8_kernel_code_hash) and that of
+the 8-bit layer operators' (tdi8_layer_code_hash).
 
 The library build also produces libtdi8_ceilings.so (roofline calibration
 kernels) and libtdi8_stamps.so: the same sources compiled with TDI8_STAMPS,
@@ -91,16 +92,22 @@ def code_object_path(obj: str, work: str) -> str:
     return os.path.join(work, os.path.basename(obj) + ".co")
 
 
-def code_object_kernels(obj: str, work: str) -> dict[str, dict]:
-    """Kernel name -> metadata (.vgpr_count, .agpr_count, ...) of the gfx950
-    code object embedded in a host object built here (the code object is left
-    at code_object_path(obj, work))."""
+def extract_code_object(obj: str, work: str) -> str:
+    """The gfx950 code object embedded in a host object built here, as a file
+    at code_object_path(obj, work)."""
     fatbin = os.path.join(work, os.path.basename(obj) + ".fatbin")
     co = code_object_path(obj, work)
     _run([os.path.join(LLVM_BIN, "llvm-objcopy"), f"--dump-section=.hip_fatbin={fatbin}", obj,
           os.path.join(work, os.path.basename(obj) + ".stripped")])
     _run([os.path.join(LLVM_BIN, "clang-offload-bundler"), "--unbundle", "--type=o",
           f"--targets=hipv4-amdgcn-amd-amdhsa--{ARCH}", f"--input={fatbin}", f"--output={co}"])
+    return co
+
+
+def code_object_kernels(obj: str, work: str) -> dict[str, dict]:
+    """Kernel name -> metadata (.vgpr_count, .agpr_count, ...) of an object's
+    code object."""
+    co = extract_code_object(obj, work)
     notes = _run([os.path.join(LLVM_BIN, "llvm-readelf"), "--notes", co])
     start = notes.index("---")
     end = notes.index("\n...", start)
@@ -108,8 +115,22 @@ def code_object_kernels(obj: str, work: str) -> dict[str, dict]:
     return {k[".name"]: k for k in meta["amdhsa.kernels"]}
 
 
+# The objects of the 8-bit layer operators' kernels, in the order of their hash.
+LAYER_OBJECTS = tuple(f"quant_rows_{ty}" for ty in ("F32", "Bf16", "F16")) + \
+    tuple(f"stream_{ty}" for ty in ("S8", "F8", "F8Wide")) + ("grouped_tiles", "block_scale_tiles")
+
+
+def layer_code_hash(bdir: str) -> str:
+    code = hashlib.sha256()
+    for name in LAYER_OBJECTS:
+        with open(extract_code_object(os.path.join(bdir, name + ".o"), bdir), "rb") as f:
+            code.update(f.read())
+    return code.hexdigest()[:16]
+
+
 def write_resource_table(objs: dict[int, str], bdir: str) -> str:
-    """Generate the C++ table of per-configuration kernel resources."""
+    """Generate the C++ table of per-configuration kernel resources, and the
+    hashes of the code objects."""
     params = config_params()
     rows = []
     code = hashlib.sha256()
@@ -131,7 +152,9 @@ def write_resource_table(objs: dict[int, str], bdir: str) -> str:
             "const KernelResources kKernelResources[TDI8_NUM_CONFIGS] = {\n" + "\n".join(rows) +
             "\n};\n\n}  // namespace tdi8\n\n"
             "// SHA-256 of the code objects of every configuration, in id order.\n"
-            'extern "C" const char *tdi8_kernel_code_hash(void) { return "' + code.hexdigest()[:16] + '"; }\n')
+            'extern "C" const char *tdi8_kernel_code_hash(void) { return "' + code.hexdigest()[:16] + '"; }\n'
+            "// The same of the 8-bit layer operators' kernels.\n"
+            'extern "C" const char *tdi8_layer_code_hash(void) { return "' + layer_code_hash(bdir) + '"; }\n')
     with open(src, "w") as f:
         f.write(text)
     return src
