@@ -272,3 +272,51 @@ def test_layer_code_hash_covers_every_layer_kernel():
     sources = {os.path.splitext(os.path.basename(p))[0] for p in glob.glob(os.path.join(b.CSRC, "*.hip"))}
     listed = {re.sub("_(S8|F8|F8Wide|F32|Bf16|F16)$", "", name) for name in b.LAYER_OBJECTS}
     assert {s.replace("stream_product", "stream") for s in sources} == listed | {"instantiate", "ceilings"}
+
+
+# ----- the package without its native calls ----------------------------------------------
+
+WITHOUT_CALLS = """
+import sys, types, warnings
+sys.path.insert(0, {root!r})
+if {other!r}:
+    calls = types.ModuleType("tiled_dense_int8_amd._calls")
+    calls.torch_version = {other!r}
+    sys.modules["tiled_dense_int8_amd._calls"] = calls
+else:
+    class Missing:
+        def find_spec(self, name, path=None, target=None):
+            if name.endswith("._calls"):
+                raise ModuleNotFoundError("no module named " + name, name=name)
+    sys.meta_path.insert(0, Missing())
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    import tiled_dense_int8_amd as t
+import torch
+assert t._calls is None and [w.category for w in seen] == [RuntimeWarning] and "_calls" in str(seen[0].message)
+assert t.tile_config_count() > 0 and t.gemm_s8s8s32(0, 4, 4, 0, 4, 0, 4, 0, 4, 0) == t.OK
+x = torch.zeros(2, 8)
+for call in (lambda: t.rms_norm(x, x[0]), lambda: t.swiglu(x, x)):
+    try:
+        call()
+    except ValueError as e:
+        assert "GPU" in str(e)
+    else:
+        raise AssertionError("not refused")
+"""
+
+
+@pytest.mark.parametrize("other", ["", "0.0.1"])
+def test_package_without_its_native_calls(other):
+    """Missing, or of another torch: the package imports with a warning and makes its calls by Python."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", WITHOUT_CALLS.format(root=root, other=other)], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+
+
+def test_native_calls_are_of_this_torch():
+    assert t._calls is not None and t._calls.torch_version == torch.__version__
