@@ -220,3 +220,63 @@ def test_inference_mode_and_leaves():
     got = t.rms_norm(x.clone().requires_grad_(), torch.nn.Parameter(w.clone()))
     same(got, want)
     assert not any(o.requires_grad for o in got)
+
+
+def operator_calls(g):
+    """(call of the outputs to write and a stream, those outputs) of every operator."""
+    x, w = normal(g, 5, 300), normal(g, 300)
+    q, q8 = torch.empty(5, 300, dtype=torch.int8).cuda(), torch.empty(5, 300, dtype=F8).cuda()
+    s, s8_ = torch.empty(5).cuda(), torch.empty(5, 3).cuda()
+    h = normal(g, 5, 300)
+    A, B, ra, rb = s8(g, 5, 64), s8(g, 30, 64), scales(g, 5), scales(g, 30)
+    A8, B8 = (normal(g, *k, dtype=torch.float32).to(F8) for k in ((5, 128), (30, 128)))
+    sa, sb = scales(g, 5, 1), scales(g, 1, 1)
+    y = torch.empty(5, 30).cuda()
+    return [
+        (lambda o, stream: t.rms_norm(x, w, residual=x, sum_out=o[0], out=o[1], scale=o[2], stream=stream), (h, q, s)),
+        (lambda o, stream: t.rms_norm(x, w, fmt="f8", out=o[0], scale=o[1], stream=stream), (q8, s8_)),
+        (lambda o, stream: t.swiglu(x, x, out=o[0], scale=o[1], stream=stream), (q, s)),
+        (lambda o, stream: t.grouped_gemm(A, ra, B, rb, out=o[0], stream=stream), (y,)),
+        (lambda o, stream: t.gemm_f8(A8, sa, B8, sb, out=o[0], stream=stream), (y,)),
+    ]
+
+
+def test_written_outputs_are_known_to_autograd():
+    """A call's outputs count as written once, made natively or by Python; those of inference mode are left alone."""
+    for call, outputs in operator_calls(gen(20)):
+        for stream in (None, torch.cuda.current_stream()):
+            before = [o._version for o in outputs]
+            call(outputs, stream)
+            assert [o._version for o in outputs] == [v + 1 for v in before]
+            with torch.inference_mode():
+                inner = [o.clone() for o in outputs]
+                call(inner, stream)
+            call(inner, stream)
+            for a, b in zip(inner, outputs):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    # the residual stream overwritten between a product and its backward pass
+    g = gen(21)
+    x, w, h = normal(g, 4, 64), normal(g, 64), normal(g, 4, 64)
+    for stream in (None, torch.cuda.current_stream()):
+        leaf = normal(g, 64).requires_grad_()
+        loss = (h * leaf).sum()
+        t.rms_norm(x, w, residual=h, sum_out=h, stream=stream)
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+
+
+def test_outputs_that_require_grad():
+    """Refused while gradients are recorded, written under no_grad as torch's own operators write them."""
+    for call, outputs in operator_calls(gen(22)):
+        want = [o.clone() for o in outputs]
+        call(want, None)
+        for k, o in enumerate(outputs):
+            if not o.dtype.is_floating_point:
+                continue
+            given = [p.clone().requires_grad_() if i == k else p for i, p in enumerate(outputs)]
+            for stream in (None, torch.cuda.current_stream()):
+                with pytest.raises(ValueError, match="requires grad"):
+                    call(given, stream)
+                with torch.no_grad():
+                    call(given, stream)
+                same(tuple(p.detach() for p in given), tuple(want))

@@ -320,3 +320,19 @@ def test_package_without_its_native_calls(other):
 
 def test_native_calls_are_of_this_torch():
     assert t._calls is not None and t._calls.torch_version == torch.__version__
+
+
+def test_outputs_that_require_grad_are_refused():
+    x, w = torch.zeros(4, 256), torch.zeros(256)
+    leaf, s = torch.zeros(4, 256, requires_grad=True), torch.zeros(4, requires_grad=True)
+    A, a, B, b = torch.zeros(4, 256, dtype=torch.int8), torch.zeros(4), torch.zeros(8, 256, dtype=torch.int8), torch.zeros(8)
+    F = x.to(torch.float8_e4m3fn)
+    y = torch.zeros(4, 8, requires_grad=True)
+    calls = (lambda: t.rms_norm(x, w, residual=x, sum_out=leaf), lambda: t.rms_norm(x, w, scale=s),
+             lambda: t.swiglu(x, x, scale=s), lambda: t.grouped_gemm(A, a, B, b, out=y),
+             lambda: t.gemm_f8(F, torch.zeros(4, 2), F[:1], torch.zeros(1, 2), out=y[:, :1]))
+    for call in calls:
+        with pytest.raises(ValueError, match="requires grad"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):  # the next check
+            call()

@@ -496,6 +496,20 @@ def _eight_bit_out(fmt, T, H, like, out, scale, stream):
     return out, ldq, scale, lds
 
 
+def _outputs(**given) -> None:
+    """Refuses outputs that autograd would take for what they were: results carry no gradients."""
+    for name, t in given.items():
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires grad, and results carry no gradients: write to it under torch.no_grad()")
+
+
+def _written(*given) -> None:
+    """The caller's outputs count as written, for backward passes that kept them."""
+    for t in given:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _vector(name, t, dtype, count) -> None:
     if t.dtype != dtype or t.shape != (count,) or (count > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a dense {dtype} vector of {count} values")
@@ -511,12 +525,17 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, fmt: str = "s8", sum_o
     fmt: "s8": q int8 with scale (T); "f8": q float8_e4m3fn with scale
        (T, ceil(H / 128)), one for each block of 128 columns.
     sum_out: where the sum goes (x or residual itself: in place).
+
+    Results carry no gradients, also where inputs require them; sum_out, out
+    and scale count as written in place for tensors that a backward pass kept.
     """
     if _calls is not None and stream is None and x.is_cuda:
         device = _current_device()
         made = _calls.rms_norm(x, weight, eps, residual, fmt, sum_out, out, scale, device, _current_stream(device))
         if made is not None:
             return made
+    _outputs(sum_out=sum_out, out=out, scale=scale)
+    given = sum_out, out, scale
     dtype = x.dtype
     code = _TYPES.get(dtype)
     if code is None:
@@ -542,17 +561,21 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, fmt: str = "s8", sum_o
         _call(index, _lib.rmsnorm_quant_s8, args, stream)
     else:
         _call(index, _lib.rmsnorm_quant_f8, args + (lds,), stream)
+    _written(*given)
     return (out, scale) if residual is None else (out, scale, sum_out)
 
 
 def swiglu(gate, up, fmt: str = "s8", out=None, scale=None, stream=None):
     """(q, scale) of gate / (1 + exp(-gate)) * up for gate and up (T, N), in
-    the formats of rms_norm; the two may be halves of one tensor's rows."""
+    the formats of rms_norm; the two may be halves of one tensor's rows.
+    Gradients as for rms_norm."""
     if _calls is not None and stream is None and gate.is_cuda:
         device = _current_device()
         made = _calls.swiglu(gate, up, fmt, out, scale, device, _current_stream(device))
         if made is not None:
             return made
+    _outputs(out=out, scale=scale)
+    given = out, scale
     dtype = gate.dtype
     code = _TYPES.get(dtype)
     if code is None:
@@ -568,6 +591,7 @@ def swiglu(gate, up, fmt: str = "s8", out=None, scale=None, stream=None):
         _call(index, _lib.swiglu_quant_s8, args, stream)
     else:
         _call(index, _lib.swiglu_quant_f8, args + (lds,), stream)
+    _written(*given)
     return out, scale
 
 
@@ -620,12 +644,16 @@ def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtyp
        outside A give zeros); without them the result has A's rows.
     out: (M, N) of a floating type, or dtype for a new tensor; rows from
        offsets[G] on are not written.
+
+    Gradients as for rms_norm.
     """
     if _calls is not None and stream is None and A.is_cuda:
         device = _current_device()
         made = _calls.grouped_gemm(A, a_scale, B, b_scale, offsets, rows, out, dtype, device, _current_stream(device))
         if made is not None:
             return made
+    _outputs(out=out)
+    given = out
     lda = _matrix("A", A, torch.int8)
     T, K = A.shape
     if B.dtype != torch.int8:
@@ -654,6 +682,7 @@ def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtyp
           (_TYPES[out.dtype], G, M, N, K, A.data_ptr(), lda, T, a_scale.data_ptr(),
            None if rows is None else rows.data_ptr(), None if offsets is None else offsets.data_ptr(), B.data_ptr(),
            ldb, B.stride(0) if G > 1 else 0, b_scale.data_ptr(), out.data_ptr(), ldc), stream)
+    _written(given)
     return out
 
 
@@ -667,12 +696,16 @@ def gemm_f8(A, a_scale, B, b_scale, out=None, dtype=torch.bfloat16, stream=None)
        float16 hold all sums in 32 bits; bfloat16 takes the e4m3 matrix
        instructions' sums, in which products below 2^-13 of the largest of
        their 16 neighbours are lost, at twice the rate.
+
+    Gradients as for rms_norm.
     """
     if _calls is not None and stream is None and A.is_cuda:
         device = _current_device()
         made = _calls.gemm_f8(A, a_scale, B, b_scale, out, dtype, device, _current_stream(device))
         if made is not None:
             return made
+    _outputs(out=out)
+    given = out
     lda = _matrix("A", A, torch.float8_e4m3fn)
     ldb = _matrix("B", B, torch.float8_e4m3fn)
     (M, K), N = A.shape, B.shape[0]
@@ -687,4 +720,5 @@ def gemm_f8(A, a_scale, B, b_scale, out=None, dtype=torch.bfloat16, stream=None)
     _call(index, _lib.gemm_f8f8_block128,
           (_TYPES[out.dtype], M, N, K, A.data_ptr(), lda, a_scale.data_ptr(), ldas, B.data_ptr(), ldb,
            b_scale.data_ptr(), ldbs, out.data_ptr(), ldc), stream)
+    _written(given)
     return out

@@ -14,6 +14,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -76,6 +77,10 @@ bool optional(PyObject *o, int64_t device, const at::Tensor *&t, bool &ok) {
     return t != nullptr;
 }
 
+// Whether a call may write the caller's tensor: not where autograd would take
+// it for what it was.
+bool writable(const at::Tensor &t) { return !t.requires_grad() || !at::GradMode::is_enabled(); }
+
 struct Output {
     at::Tensor made;          // a new one
     PyObject *given = nullptr;
@@ -93,8 +98,12 @@ struct Output {
         data = made.data_ptr();
         ld = shape.back() > 1 ? shape.back() : 1;
     }
+    // The result.  The caller's tensor counts as written, for backward passes
+    // that kept it.
     PyObject *object() {
         if (!given) return THPVariable_Wrap(std::move(made));
+        const at::Tensor &t = THPVariable_Unpack(given);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
         Py_INCREF(given);
         return given;
     }
@@ -109,12 +118,12 @@ bool eight_bit_out(bool f8, int64_t T, int64_t H, const at::Tensor &like, PyObje
     const at::Tensor *tq, *ts;
     if (optional(out, device, tq, ok)) {
         const int64_t ld = matrix(*tq, type, T, H);
-        if (ld < 0) return false;
+        if (ld < 0 || !writable(*tq)) return false;
         q.take(out, *tq, ld);
     }
     if (optional(scale, device, ts, ok)) {
         const int64_t ld = f8 ? matrix(*ts, ScalarType::Float, T, blocks) : 1;
-        if (ld < 0 || (!f8 && !vector(*ts, ScalarType::Float, T))) return false;
+        if (ld < 0 || (!f8 && !vector(*ts, ScalarType::Float, T)) || !writable(*ts)) return false;
         s.take(scale, *ts, ld);
     }
     if (!ok) return false;
@@ -188,7 +197,7 @@ PyObject *rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Output o[3];  // q, scale, sum
     if (in_place) {
         const int64_t ld = matrix(*given_sum, dtype, T, H);
-        if (ld < 0) Py_RETURN_NONE;
+        if (ld < 0 || !writable(*given_sum)) Py_RETURN_NONE;
         o[2].take(a[5], *given_sum, ld);
     }
     if (!eight_bit_out(fmt == 1, T, H, *x, a[6], a[7], w.device, o[0], o[1])) Py_RETURN_NONE;
@@ -246,7 +255,7 @@ int product_out(PyObject *out, PyObject *dtype, int64_t M, int64_t N, const at::
     if (optional(out, device, given, ok)) {
         const int type = type_of(given->scalar_type());
         const int64_t ld = matrix(*given, given->scalar_type(), M, N);
-        if (type < 0 || ld < 0) return -1;
+        if (type < 0 || ld < 0 || !writable(*given)) return -1;
         c.take(out, *given, ld);
         return type;
     }
