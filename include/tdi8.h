@@ -435,8 +435,9 @@ int swiglu_quant_f8(int type, int T, int N, const void *gate, int ldg, const voi
  * 64 x 128 results, each group's rows filled up to 64 (scaled_product_plan
  * says so beforehand).
  * C may not overlap an input (TDI8_ERR_ALIASING).
- * M, N or G = 0 enqueues nothing; K = 0 writes zeros.  16-byte aligned A and B
- * with lda, ldb, group_b and K multiples of 16 take the faster kernels.
+ * M, N or G = 0 enqueues nothing; K = 0 writes zeros, whatever the scales.
+ * 16-byte aligned A and B with lda, ldb, group_b and K multiples of 16 take
+ * the faster kernels.
  * Ownership, streams and the other errors as for gemm_s8s8s32. */
 int gemm_s8s8_grouped(int type, int G, int M, int N, int K, const int8_t *A, int lda, int a_rows,
                       const float *a_scale, const int32_t *rows, const int32_t *offsets, const int8_t *B, int ldb,

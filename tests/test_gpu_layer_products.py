@@ -543,3 +543,18 @@ def test_f8_bf16_sums_of_loud_channels(size):
         off = (got.cpu().double() - want).abs()
         absolute = pieces * (15 / 16) * 2.0 ** -13 + size_of * 2.0 ** -15
         assert (off <= absolute * (1 + 2.0 ** -8) + want.abs() * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_empty_sums_are_zero_whatever_their_scales(bad):
+    """K = 0 in every kernel that the sizes take, with scales that are no numbers."""
+    for counts, N in (([2, 0, 3], 5), ([40, 30], 300), ([300, 500], 2000), ([3], 7), ([70], 3999), ([3000], 4096)):
+        M, G = sum(counts), len(counts)
+        off = torch.tensor([0] + counts).cumsum(0).int().cuda()
+        for lda in (16, 17):
+            note(f"[case] no K {counts} N={N} lda={lda}")
+            A = torch.zeros(M, lda, dtype=torch.int8, device="cuda")[:, :0]
+            B = torch.zeros(G, N, lda, dtype=torch.int8, device="cuda")[:, :, :0]
+            out = torch.full((M + 2, N), SENTINEL, device="cuda")
+            t.grouped_gemm(A, torch.full((M,), bad).cuda(), B, torch.full((G, N), bad).cuda(), off, out=out[:M])
+            assert (out[:M] == 0).all() and (out[M:] == SENTINEL).all()

@@ -229,6 +229,8 @@ int product_entry(bool f8, ProductArgs g, hipStream_t stream) {
     if (!choose_product(f8, g.type, g.G, g.M, g.N, g.K, al, near, units, &c)) return TDI8_ERR_INVALID_VALUE;
     g.tiles_m = c.tiles_m;
     g.tiles_n = c.tiles_n;
+    // an empty sum is zero, whatever its scales: no row counts as inside A
+    if (g.K == 0) g.a_rows = 0;
     const ProductKernels &pk = *product_kernels(f8, g.type);
     const void *kernel = c.form == TDI8_SCALED_STREAM             ? pk.stream[c.index]
                          : c.form == TDI8_SCALED_STREAM_UNALIGNED ? (c.index == kGroupStream ? pk.unaligned_group
