@@ -358,7 +358,9 @@ int conv2d_validate(int N, int H, int W, int C, int K, int R, int S,
  * f8 scales of the activation, and of the norm of 32-bit values, come from the
  * 32-bit form of the largest value and are off by less than 2^-20.
  * A row (f8: a block) of zeros gets q = 0 and scale = 0; one that holds an
- * infinity or NaN gets q = 0 and scale = NaN.
+ * infinity or NaN gets q = 0 and scale = NaN.  In the norm an infinity makes
+ * the row's other values zeros, NaN makes them NaN: the f8 blocks beside it get
+ * q = 0 and scale = 0 or NaN.
  *
  * Types of x, residual, weight, sum, gate and up: */
 typedef enum {

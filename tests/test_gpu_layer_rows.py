@@ -323,3 +323,23 @@ def test_act_far_values_beside_small_ones(kind, fmt):
             q, scale = t.swiglu(gate.cuda(), up.cuda(), fmt=fmt)
             v, inv = act_values(gate, up)
             check_quantised(q, scale, v, inv, fmt, what)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("H", [300, 2500, 20000])
+def test_f8_norm_blocks_beside_an_infinity_or_nan(kind, H):
+    """Values over a root that is infinite are zeros, over one that is NaN are NaN: of blocks of zeros too."""
+    g = gen(12)
+    x = torch.randn(4, H, generator=g).to(TYPES[kind])
+    x[:, 128:200] = 0
+    x[:, 256:] = x[:, 256:] * (torch.arange(256, H) % 2)
+    x[1, 5], x[2, 5], x[3, 5] = float("inf"), float("nan"), float("-inf")
+    w = (1 + torch.rand(H, generator=g)).to(TYPES[kind])
+    x[:, 200:256] = 0  # block 1 holds only zeros
+    for residual in (None, torch.zeros_like(x).cuda()):
+        made = t.rms_norm(x.cuda(), w.cuda(), residual=residual, fmt="f8")
+        q, scale = made[0].cpu().float(), made[1].cpu()
+        assert (q[1:] == 0).all() and q[0].abs().max() == 448
+        assert scale[0].isfinite().all() and scale[0, 1] == 0 and scale[0, 0] > 0
+        assert scale[1:, 0].isnan().all()
+        assert (scale[[1, 3], 1:] == 0).all() and scale[2].isnan().all()

@@ -21,6 +21,8 @@
 //
 // A row (f8: block) that holds an infinity or NaN has q = 0 and scale = NaN,
 // so that products with it come out NaN; one of zeros has q = 0 and scale = 0.
+// The other f8 blocks of a norm's row that holds one are values over the row's
+// root: zeros over an infinity, NaN over NaN.
 //
 // Bound by memory: 3 T-sized streams and 1 byte per element (norm with a
 // residual), read and written once.  A row stays in registers between its
@@ -597,6 +599,7 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
         if (t == 0) g.scale[row] = scale_of(m, root(), 127.0, number);
     } else {
         const double inv = root();
+        const bool rooted = OP != kOpNorm || sum < __builtin_inf();
         each([&](int v, const float *f, auto &&operands) {
             const int c = col0 + (v * THREADS + t) * 8;
             const int n = g.cols - c;
@@ -656,6 +659,10 @@ __global__ void __launch_bounds__(THREADS == 64 ? 256 : THREADS) quant_rows_kern
                 w2[1] = static_cast<uint32_t>(q >> 32);
             }
             if (n <= 0) return;
+            if (!rooted) {
+                w2[0] = w2[1] = 0;
+                number = number && sum == sum;
+            }
             if ((t & 15) == 0) g.scale[row * g.lds + (c >> 7)] = scale_of(m, inv, 448.0, number);
             store8_bytes(pq + c, w2[0], w2[1], n);
         });
