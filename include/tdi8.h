@@ -414,7 +414,8 @@ int swiglu_quant_f8(int type, int T, int N, const void *gate, int ldg, const voi
  * i = rows[r] (or r itself when rows is NULL), the sum exact in int32 and the
  * result rounded to `type` once (fp32 in between: the sum, the scales'
  * product and their product are rounded to 24 bits each).
- *   A        a_rows rows of K int8, leading dimension lda; a_scale a_rows floats
+ *   A        a_rows rows of K int8 (one at least), leading dimension lda;
+ *            a_scale a_rows floats
  *   rows     M indices of A's rows, in group order (a router's sorted token
  *            list; an index may occur any number of times), or NULL
  *   offsets  G + 1 rising row numbers on the device, offsets[0] = 0,
@@ -430,7 +431,7 @@ int swiglu_quant_f8(int type, int T, int N, const void *gate, int ldg, const voi
  * host: the call only enqueues one kernel, and may be captured into a graph
  * whose replays see other offsets.
  * K is at most 131071 (no sum can wrap) and the other sizes at most 2^30; a
- * group_b below one group's extent, a_rows < M without rows, an unknown type
+ * group_b below one group's extent, a_rows < M without rows, a_rows = 0, an unknown type
  * or pointers that are not aligned to their element give
  * TDI8_ERR_INVALID_VALUE, and so does a product whose grid would pass 2^31
  * threads in every tile that its operands allow: never below 4 * 10^6 tiles of

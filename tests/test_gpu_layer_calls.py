@@ -280,3 +280,17 @@ def test_outputs_that_require_grad():
                 with torch.no_grad():
                     call(given, stream)
                 same(tuple(p.detach() for p in given), tuple(want))
+
+
+def test_operands_that_lie_wrong():
+    """Refused in words on the GPU as well, where the native calls leave them to Python."""
+    g = gen(23)
+    A, s, B, bs = s8(g, 4, 64), scales(g, 4), s8(g, 3, 8, 64), scales(g, 3, 8)
+    off, rows = torch.tensor([0, 1, 2, 4], dtype=torch.int32).cuda(), torch.zeros(5, dtype=torch.int32).cuda()
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(ValueError, match="groups overlap"):
+            t.grouped_gemm(A, s, B[:1].expand(3, 8, 64), bs, off, stream=stream)
+        with pytest.raises(ValueError, match="rows overlap"):
+            t.grouped_gemm(A, s, torch.as_strided(B, (3, 8, 64), (512, 63, 1)), bs, off, stream=stream)
+        with pytest.raises(ValueError, match="no rows"):
+            t.grouped_gemm(A[:0], s[:0], B, bs, off, rows=rows, stream=stream)

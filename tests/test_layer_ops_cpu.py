@@ -336,3 +336,23 @@ def test_outputs_that_require_grad_are_refused():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="GPU"):  # the next check
             call()
+
+
+def test_operands_that_lie_wrong_are_refused_in_words():
+    A, s = torch.zeros(4, 256, dtype=torch.int8), torch.zeros(4)
+    B, bs = torch.zeros(3, 8, 256, dtype=torch.int8), torch.zeros(3, 8)
+    off, rows = torch.zeros(4, dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+    with pytest.raises(ValueError, match="groups overlap"):
+        t.grouped_gemm(A, s, B[:1].expand(3, 8, 256), bs, off)
+    with pytest.raises(ValueError, match="groups overlap"):
+        t.grouped_gemm(A, s, torch.as_strided(B, (3, 8, 256), (255 + 7 * 256, 256, 1)), bs, off)
+    with pytest.raises(ValueError, match="rows overlap"):
+        t.grouped_gemm(A, s, torch.as_strided(B, (3, 8, 256), (2048, 255, 1)), bs, off)
+    with pytest.raises(ValueError, match="no rows"):
+        t.grouped_gemm(A[:0], s[:0], B, bs, off, rows=rows)
+    # what lies apart, and calls of no rows, go on to the next check
+    for args in ((A, s, torch.zeros(3, 9, 272, dtype=torch.int8)[:, :8, :256], bs, off),
+                 (A[:0], s[:0], B[:1].expand(3, 8, 256), bs, off), (A[:0], s[:0], B, bs, off, rows[:0]),
+                 (A[:, :0], s, B[:, :, :0], bs, off)):
+        with pytest.raises(ValueError, match="GPU"):
+            t.grouped_gemm(*args)

@@ -638,10 +638,13 @@ def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtyp
     a_scale[i] * b_scale[g] * (A[i] x B[g] transposed) with i = rows[r] or r.
 
     A: int8 (T, K); a_scale: float32 (T), as rms_norm and swiglu give them.
-    B: int8 (G, N, K) with b_scale float32 (G, N), or (N, K) with (N).
+    B: int8 (G, N, K) with b_scale float32 (G, N), or (N, K) with (N).  Groups
+       and rows may lie apart but not overlap (no weights shared by a zero
+       stride).
     offsets: int32 (G + 1) on the GPU (not needed for one group of all rows).
     rows: int32 row indices into A, one for each row of the result (rows
-       outside A give zeros); without them the result has A's rows.
+       outside A give zeros, but A has one row at least); without them the
+       result has A's rows.
     out: (M, N) of a floating type, or dtype for a new tensor; rows from
        offsets[G] on are not written.
 
@@ -674,9 +677,16 @@ def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtyp
     if rows is not None:
         M = rows.numel()
         _vector("rows", rows, torch.int32, M)
+    ldb = B.stride(1) if N > 1 else max(K, 1)
+    if M > 0 and N > 0 and G > 0:
+        if T == 0:
+            raise ValueError("A has no rows for `rows` to name")
+        if ldb < K:
+            raise ValueError("B's rows overlap")
+        if G > 1 and B.stride(0) < (N - 1) * ldb + K:
+            raise ValueError("B's groups overlap: weights that groups share need a copy for each")
     index = _gpu(A, a_scale, B, b_scale, offsets, rows, out)
     out, ldc = _product_out(M, N, dtype, A, out, stream)
-    ldb = B.stride(1) if N > 1 else max(K, 1)
     _fit(G, M, N, K, lda, T, ldb, ldc)
     _call(index, _lib.gemm_s8s8_grouped,
           (_TYPES[out.dtype], G, M, N, K, A.data_ptr(), lda, T, a_scale.data_ptr(),

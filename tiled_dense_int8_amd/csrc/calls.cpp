@@ -288,6 +288,8 @@ PyObject *grouped_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t M = rows ? rows->numel() : T;
     if (rows && !vector(*rows, ScalarType::Int, M)) Py_RETURN_NONE;
     const int64_t ldb = N > 1 ? B->stride(1 - one) : K > 1 ? K : 1, group_b = G > 1 ? B->stride(0) : 0;
+    // (operands that the library refuses for how they lie, which Python puts into words)
+    if (M > 0 && (T == 0 || ldb < K || (G > 1 && group_b < (N - 1) * ldb + K))) Py_RETURN_NONE;
     Output c;
     const int type = product_out(a[6], a[7], M, N, *A, w.device, c);
     if (type < 0 || !fit(G, M, N, K, lda, T, ldb, c.ld)) Py_RETURN_NONE;
