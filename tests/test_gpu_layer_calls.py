@@ -294,3 +294,15 @@ def test_operands_that_lie_wrong():
             t.grouped_gemm(A, s, torch.as_strided(B, (3, 8, 64), (512, 63, 1)), bs, off, stream=stream)
         with pytest.raises(ValueError, match="no rows"):
             t.grouped_gemm(A[:0], s[:0], B, bs, off, rows=rows, stream=stream)
+
+
+def test_lazily_negated_operands_are_refused():
+    x, w = torch.ones(4, 1, device="cuda"), torch.ones(1, device="cuda")
+    column = torch.full((4, 1), 1 + 1j, device="cuda").conj().imag
+    q, scale = torch.empty(4, 1, dtype=torch.int8, device="cuda"), torch._neg_view(torch.empty(4, device="cuda"))
+    for stream in (None, torch.cuda.current_stream()):
+        for call in (lambda: t.rms_norm(column, w, stream=stream), lambda: t.rms_norm(x, w, scale=scale, stream=stream),
+                     lambda: t.swiglu(x, column, out=q, stream=stream)):
+            with pytest.raises(ValueError, match="negated lazily"):
+                call()
+    same(t.rms_norm(column.resolve_neg(), w), t.rms_norm(-x, w))

@@ -356,3 +356,28 @@ def test_operands_that_lie_wrong_are_refused_in_words():
                  (A[:, :0], s, B[:, :, :0], bs, off)):
         with pytest.raises(ValueError, match="GPU"):
             t.grouped_gemm(*args)
+
+
+def negated(t_):
+    """A view whose memory holds the values of the other sign."""
+    view = torch._neg_view(t_)
+    assert view.is_neg() or not t_.numel()
+    return view
+
+
+def test_lazily_negated_operands_are_refused():
+    """Their memory holds other values than they show."""
+    x, w, n = torch.ones(4, 256), torch.ones(256), negated
+    column = torch.ones(4, 1, dtype=torch.complex64).conj().imag  # as ordinary code comes by one
+    assert column.is_neg()
+    A, a, B, b = torch.ones(4, 256, dtype=torch.int8), torch.ones(4), torch.ones(8, 256, dtype=torch.int8), torch.ones(8)
+    F, f, g = x.to(torch.float8_e4m3fn), torch.ones(4, 2), torch.ones(1, 2)
+    calls = [lambda: t.rms_norm(column, torch.ones(1)), lambda: t.swiglu(x[:, :1], column),
+             lambda: t.rms_norm(n(x), w), lambda: t.rms_norm(x, n(w)), lambda: t.rms_norm(x, w, residual=n(x)),
+             lambda: t.rms_norm(x, w, residual=x, sum_out=n(x)), lambda: t.swiglu(n(x), x), lambda: t.swiglu(x, n(x)),
+             lambda: t.grouped_gemm(n(A), a, B, b), lambda: t.grouped_gemm(A, n(a), B, b),
+             lambda: t.grouped_gemm(A, a, n(B), b), lambda: t.grouped_gemm(A, a, B, n(b)),
+             lambda: t.gemm_f8(F, n(f), F, g), lambda: t.gemm_f8(F, f, F, n(g))]
+    for call in calls:
+        with pytest.raises(ValueError, match="negated lazily"):
+            call()

@@ -442,10 +442,17 @@ def _fit(*values) -> None:
         raise ValueError(f"a size or stride of {max(values)} does not fit the library's int arguments (< 2**31)")
 
 
+def _stored(name, t) -> None:
+    """Refuses a tensor whose memory holds something else than its values."""
+    if t.is_neg():
+        raise ValueError(f"{name} is negated lazily: pass its resolve_neg()")
+
+
 def _matrix(name, t, dtype, shape=None) -> int:
     """Checks a 2-D tensor with unit column stride; its leading dimension."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    _stored(name, t)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with unit column stride")
     rows, cols = size = t.shape
@@ -513,6 +520,7 @@ def _written(*given) -> None:
 def _vector(name, t, dtype, count) -> None:
     if t.dtype != dtype or t.shape != (count,) or (count > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a dense {dtype} vector of {count} values")
+    _stored(name, t)
 
 
 def rms_norm(x, weight, eps: float = 1e-6, residual=None, fmt: str = "s8", sum_out=None, out=None, scale=None,
@@ -661,6 +669,8 @@ def grouped_gemm(A, a_scale, B, b_scale, offsets=None, rows=None, out=None, dtyp
     T, K = A.shape
     if B.dtype != torch.int8:
         raise TypeError(f"B must be torch.int8, not {B.dtype}")
+    _stored("B", B)
+    _stored("b_scale", b_scale)
     if B.dim() == 2:
         B, b_scale = B[None], b_scale[None]
     if B.dim() != 3 or B.shape[2] != K or (K > 1 and B.stride(2) != 1):

@@ -46,11 +46,13 @@ int type_of(ScalarType t) {
                                                                          : -1;
 }
 
-// A dense tensor on GPU `device`, or null.
+// A dense tensor on GPU `device` whose memory holds its values (no lazy
+// negation), or null.
 const at::Tensor *tensor(PyObject *o, int64_t device) {
     if (!THPVariable_CheckExact(o)) return nullptr;
     const at::Tensor &t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.get_device() != device || t.layout() != at::kStrided) return nullptr;
+    if (!t.is_cuda() || t.get_device() != device || t.layout() != at::kStrided || t.is_neg())
+        return nullptr;
     return &t;
 }
 
