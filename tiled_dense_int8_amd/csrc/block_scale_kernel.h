@@ -31,10 +31,10 @@
 // Measured on MI355X: 4096^3 to bf16 72 to 77 us (1.8 PFLOP/s), 8192^3 500 to
 // 550 us (2.1 PFLOP/s; the range is that of the chip's clock from one machine
 // to the next; a plain e4m3 product of that size without scales reaches 2.6),
-// to fp32 4096^3 129 us.  At 8192^3 the matrix cores are busy 57% of the
-// cycles at 1.63 GHz, the clock that power allows; LDS reads and DMA writes
-// take as many cycles as the matrix work beside them ((128 + 64) rows read for
-// 128 x 64 results a wave; wider wave tiles need more accumulators than a
+// to fp32 4096^3 127 to 135 us.  At 8192^3 the matrix cores are busy 47% of
+// the cycles at 2.1 GHz, the vector units 37%, LDS reads 22%: none is full, and
+// each of the two waves of a SIMD waits 31% of its time ((128 + 64) rows read
+// for 128 x 64 results a wave; wider wave tiles need more accumulators than a
 // wave has registers that multiply-adds can address).  Tiles: 256 x 256 of two
 // stages for many rows; 128 x 128 twice on a compute unit, or with four
 // stages once; 64 x 128 with four (product_table.h has their costs).

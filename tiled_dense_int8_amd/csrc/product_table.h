@@ -9,7 +9,10 @@ namespace tdi8 {
 
 // Tiles of a kernel, and what a product of them was measured to take: start
 // microseconds, and for each round of `per_cu` blocks on every compute unit
-// fixed + per_4096 * K / 4096.
+// fixed + per_4096 * K / 4096.  They rank the tiles of one product; they do not
+// foretell its time, having no term for bytes from HBM (8 groups of 32 rows,
+// 28672 x 4096 int8: 115 us by the table, 182 for reading B) nor for what long
+// sums gain (4096 x 4096 x 4095 e4m3, staged: 229 us by the table, 172 measured).
 struct Tile {
     int bm, bn, threads;
     int per_cu;
@@ -53,8 +56,8 @@ constexpr Tile kStagedTile[kStagedTiles] = {{64, 128, 512, 1, 0.0f, 2.2f, 46.0f}
 
 // Operand types of the kernels.  e4m3 products take the matrix instruction's
 // own sums for bf16 results only: they can be off by half a step of fp16
-// (operand_types.h).  With fp16 and fp32 results e4m3 is widened (on one card
-// 4096^3 144 us to fp16, 89 to bf16; 16 x 4096 x 4096 5.4 and 5.2).
+// (operand_types.h).  With fp16 and fp32 results e4m3 is widened (4096^3 127
+// us to fp16, 71 to bf16; 256 x 4096 x 4096 14.1 and 11.6, 16 rows 5.4 and 5.2).
 enum { kProductS8 = 0, kProductF8 = 1, kProductF8Wide = 2 };
 inline int product_type(bool f8, int type) {
     return !f8 ? kProductS8 : type == TDI8_BF16 ? kProductF8 : kProductF8Wide;

@@ -34,8 +34,11 @@
 // Measured on MI355X (bytes read and written once over the time; a device
 // copy of 1 GiB runs at 5.2 TB/s): norm of 16384 x 8192 bf16 with a residual
 // 162 us (5.8 TB/s) s8, 163 us f8; 4096 x 16384 89 us (5.3 TB/s); 2048 x 20000,
-// read twice, 94 us (3.1 TB/s).  act of 8192 x 11008 bf16 118 us (3.8 TB/s)
-// s8, 100 us (4.5 TB/s) f8: there the exponential's instructions count.  A
+// read twice, 84 us (3.4 TB/s) s8, 73 us f8.  act of 8192 x 11008 bf16 118 us
+// (3.8 TB/s) s8, 100 us (4.5 TB/s) f8: there the vector units count, active in
+// 69% (s8) and 89% (f8) of the cycles.  Both execute the same number of
+// instructions within 3%; s8's waves wait longer (57% of their cycles against 37%), for
+// the row's two reductions across a block of 512 threads, which f8 has not.  A
 // single row of 4096 columns takes 3 us, most of it the launch.
 #pragma once
 
