@@ -487,7 +487,7 @@ def test_more_columns_than_the_smallest_tile_has_a_grid_for(kind):
     want = sum(B[:, k].float() * A[0, k].float() for k in range(K)).to(TYPES[kind])
     got = t.grouped_gemm(A, ones[:1], B, ones, dtype=TYPES[kind])
     assert torch.equal(got[0], want)
-    # e4m3: the values 1 .. 8, so that 16 of their products keep within the instruction's 13 bits
+    # e4m3: the values 1 .. 8, so that 8 of their products keep within the instruction's 13 bits
     A8, B8 = ((x & 7).float() + 1 for x in (A, B))
     want = sum(B8[:, k] * A8[0, k] for k in range(K)).to(TYPES[kind])
     A8, B8 = A8.to(torch.float8_e4m3fn), B8.to(torch.float8_e4m3fn)
@@ -536,25 +536,38 @@ def test_f8_bf16_sums_of_loud_channels(size):
         A = A.clamp(-448, 448).to(torch.float8_e4m3fn)
         sa, sb = scales(g, M, -(-K // 128)), scales(g, -(-N // 128), -(-K // 128))
         got = t.gemm_f8(A.cuda(), sa.cuda(), B.cuda(), sb.cuda())
-        want, size_of, pieces = f8_reference(A, sa, B, sb)
-        # 15 of 16 products of a piece, each by less than 2^-13 of the piece's
-        # largest, whose bound `pieces` counts 16 times; sums in 32 bits and
-        # the type's rounding as check_f8 has them (127 * 2^-23 + 40 * 2^-24 < 2^-15)
+        want, size_of, _ = f8_reference(A, sa, B, sb)
+        # 7 of 8 consecutive products, each by less than 2^-13 of the largest of
+        # them; sums in 32 bits and the type's rounding as check_f8 has them
+        # (127 * 2^-23 + 40 * 2^-24 < 2^-15)
+        largest = [torch.nn.functional.pad(x.double().abs() * s.double().repeat_interleave(128, 1)[:, :K].abs(),
+                                           (0, -K % 8)).view(x.shape[0], -1, 8).amax(2)
+                   for x, s in ((A, sa), (B, sb.repeat_interleave(128, 0)[:N]))]
         off = (got.cpu().double() - want).abs()
-        absolute = pieces * (15 / 16) * 2.0 ** -13 + size_of * 2.0 ** -15
+        absolute = 7 * largest[0] @ largest[1].t() * 2.0 ** -13 + size_of * 2.0 ** -15
         assert (off <= absolute * (1 + 2.0 ** -8) + want.abs() * 2.0 ** -8).all()
 
 
-@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_empty_sums_are_zero_whatever_their_scales(bad):
-    """K = 0 in every kernel that the sizes take, with scales that are no numbers."""
-    for counts, N in (([2, 0, 3], 5), ([40, 30], 300), ([300, 500], 2000), ([3], 7), ([70], 3999), ([3000], 4096)):
-        M, G = sum(counts), len(counts)
-        off = torch.tensor([0] + counts).cumsum(0).int().cuda()
-        for lda in (16, 17):
-            note(f"[case] no K {counts} N={N} lda={lda}")
-            A = torch.zeros(M, lda, dtype=torch.int8, device="cuda")[:, :0]
-            B = torch.zeros(G, N, lda, dtype=torch.int8, device="cuda")[:, :, :0]
-            out = torch.full((M + 2, N), SENTINEL, device="cuda")
-            t.grouped_gemm(A, torch.full((M,), bad).cuda(), B, torch.full((G, N), bad).cuda(), off, out=out[:M])
-            assert (out[:M] == 0).all() and (out[M:] == SENTINEL).all()
+def test_f8_bf16_products_beside_a_loud_one():
+    """What a product of 448^2 does to small ones in bf16 results: cut toward
+    zero to multiples of 8 among the same 8 consecutive ones, kept elsewhere.
+    The loud one is taken back in the next block of 128, where sums are fp32."""
+    M, K = 256, 256
+    for loud in (0, 5, 15, 40, 127):
+        for small in (1.0, -3.0, 8.0, 9.0, -15.0, 44.0):
+            a, b = torch.zeros(M, K), torch.zeros(16, K)
+            a[torch.arange(128), torch.arange(128)] = small
+            a[:, loud], a[:, 128] = 448, -448
+            b[:, :128], b[:, loud], b[:, 128] = 1, 448, 448
+            one = torch.ones(M, 2).cuda()
+            a, b = (x.to(torch.float8_e4m3fn).cuda() for x in (a, b))
+            want = torch.full((128,), small)
+            want[loud // 8 * 8:loud // 8 * 8 + 8] = float(torch.tensor(small / 8).trunc()) * 8
+            want[loud] = 0  # the loud one itself
+            got = t.gemm_f8(a, one, b, one[:1])
+            assert torch.equal(got[:128].float().cpu(), want[:, None].expand(128, 16))
+            want = torch.full((128,), small)
+            want[loud] = 0
+            for kind in (torch.float16, torch.float32):  # sums in 32 bits
+                got = t.gemm_f8(a, one, b, one[:1], dtype=kind)
+                assert torch.equal(got[:128].float().cpu(), want[:, None].expand(128, 16))

@@ -77,18 +77,20 @@ struct Operand<S8> {
 
 // e4m3: one v_mfma_f32_16x16x128_f8f6f4, whose 128 products of K are exactly a
 // scale block, then acc += scale * part in fp32.
-// The instruction adds the 16 products of a 16-byte piece after cutting each,
-// toward zero, to a multiple of 2^-13 of the largest one's power of two
-// (measured: 2^5 + 2^-8 is exact within a piece, 2^6 + 2^-8 gives 2^6; between
-// pieces sums are fp32).  So a result is off by at most 15 * 2^-13 times the
-// sum of the pieces' largest magnitudes.  By that rule (emulated, K = 4096) it
-// is off by 2.8 * 10^-5 of the results' root mean square on normal operands
-// (10^-4 at worst), by 10^-4 with a channel 30 times louder in each block (4 to
-// 6 * 10^-4 at worst); where all products have one sign and one of each 16 is
-// far the largest, a result loses 5 * 10^-4 of itself, and never 2^-9, half a
-// step of bf16; where large products cancel, what is left can be lost.  For bf16 results the full rate is taken
-// for that: an e4m3 operand itself is rounded by up to 2^-4 of a value, the
-// products that are cut among them.  Half a step of fp16 (2^-12) it can reach.
+// The instruction adds 8 consecutive products after cutting each, toward zero,
+// to a multiple of 2^-13 times 2^e, e the largest sum of two operands' exponents
+// among the 8 (measured: beside 448 * 448 = 3.1 * 2^16 the 7 others are cut to
+// multiples of 8, those of the next 8 are kept; 2^5 + 2^-8 is exact, 2^6 + 2^-8
+// gives 2^6); between the eights sums are fp32.  So a result is off by at most 7
+// * 2^-13 times the sum of the eights' largest products.  By that rule
+// (emulated, K = 4096) it is off by 1.5 * 10^-5 of the results' root mean square
+// on normal operands (5 * 10^-5 at worst), by 3.5 * 10^-5 with a channel 30
+// times louder in each block (1.5 * 10^-4 at worst); where all products have one
+// sign and one of each 8 is far the largest, a result loses up to 3.6 * 10^-4 of
+// itself, and never 2^-10, a quarter of a step of bf16; where large products
+// cancel, what is left can be lost.  For bf16 results the full rate is taken for
+// that: an e4m3 operand itself is rounded by up to 2^-4 of a value, the products
+// that are cut among them.  Half a step of fp16 (2^-12) it can reach.
 template <>
 struct Operand<F8> {
     i32x8 v;
