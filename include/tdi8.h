@@ -431,13 +431,12 @@ int swiglu_quant_f8(int type, int T, int N, const void *gate, int ldg, const voi
  * host: the call only enqueues one kernel, and may be captured into a graph
  * whose replays see other offsets.
  * K is at most 131071 (no sum can wrap) and the other sizes at most 2^30; a
- * group_b below one group's extent, a_rows < M without rows, a_rows = 0, an unknown type
- * or pointers that are not aligned to their element give
+ * group_b below one group's extent, a_rows < M without rows, a_rows = 0, an
+ * unknown type or pointers that are not aligned to their element give
  * TDI8_ERR_INVALID_VALUE, and so does a product whose grid would pass 2^31
  * threads in every tile that its operands allow: never below 4 * 10^6 tiles of
  * 64 x 128 results, each group's rows filled up to 64 (scaled_product_plan
- * says so beforehand).
- * C may not overlap an input (TDI8_ERR_ALIASING).
+ * says so beforehand).  C may not overlap an input (TDI8_ERR_ALIASING).
  * M, N or G = 0 enqueues nothing; K = 0 writes zeros, whatever the scales.
  * 16-byte aligned A and B with lda, ldb, group_b and K multiples of 16 take
  * the faster kernels.
@@ -486,9 +485,10 @@ typedef struct {
 
 /* What gemm_s8s8_grouped (f8 = 0) or gemm_f8f8_block128 (f8 = 1, G = 1) would
  * enqueue for these sizes on a device of num_cu compute units; aligned: A, B,
- * lda, ldb, group_b and K are multiples of 16.  TDI8_ERR_INVALID_VALUE where
- * the call would give it for its sizes.  Needs no device; the calls take the
- * same decision. */
+ * lda, ldb, group_b and K are multiples of 16 (and leading dimensions of e4m3
+ * operands below 8 * 10^6, beyond which the LDS tiles do not address them).
+ * TDI8_ERR_INVALID_VALUE where the call would give it for its sizes.  Needs no
+ * device; the calls take the same decision. */
 int scaled_product_plan(int f8, int type, int G, int M, int N, int K, int aligned, int num_cu, tdi8_scaled_plan *out);
 
 /* Host-side argument check shared by every gemm entry point (no device

@@ -167,7 +167,8 @@ def calls_unit(out: str) -> list[str]:
     # as torch.__version__ says it, without importing torch
     with open(os.path.join(torch_dir, "version.py")) as f:
         version = re.search(r"^__version__ = '([^']+)'", f.read(), flags=re.M).group(1)
-    return [CXX, f'-DTDI8_TORCH_VERSION="{version}"', "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-I", INCLUDE,
+    return [CXX, f'-DTDI8_TORCH_VERSION="{version}"', "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-fvisibility=hidden", "-Wall", "-I", INCLUDE,
             "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
             "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.cpp"),
             "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", out]

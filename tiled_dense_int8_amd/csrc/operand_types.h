@@ -108,8 +108,8 @@ struct Operand<F8> {
     }
 };
 
-// For fp32 and fp16 results: e4m3 widened to bf16 (exact), whose products are added in
-// fp32: v_mfma_f32_16x16x32_bf16, four a chunk, at half the rate.
+// For fp32 and fp16 results: e4m3 widened to bf16 (exact), whose products are
+// added in fp32: v_mfma_f32_16x16x32_bf16, four a chunk, at half the rate.
 template <>
 struct Operand<F8Wide> {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
